@@ -77,6 +77,8 @@ struct CUstream_st;
 #define SPECDEC_MAX_TREE_NODES 1024 /* N + 1, root included */
 #define SPECDEC_MAX_DEPTH 32
 #define SPECDEC_MAX_TOPK 8
+#define SPECDEC_MAX_BEAMS 32              /* beams of a request, and beams selected */
+#define SPECDEC_MAX_PLAN_ROWS (1 << 24)   /* rows of a request in specdec_plan_slots, positions of a page */
 
 typedef enum {
     SPECDEC_OK = 0,
@@ -409,6 +411,119 @@ specdec_status specdec_shard_rejection_finish(const int32_t* gathered_tokens, in
 specdec_status specdec_ngram_propose(const int32_t* tokens, int64_t token_stride, const int32_t* lengths, int B,
                                      int n_min, int n_max, int k, int32_t* drafts, int32_t* num_drafts,
                                      int32_t* draft_offsets, int32_t* packed_drafts, struct CUstream_st* stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the verify step: growing the drafts, and the caches of the requests.
+ * ------------------------------------------------------------------------- */
+
+/* Beam selection: one step of beam search, or one level of a draft tree whose
+ * branches are kept by cumulative probability (handbook page, "EAGLE": the
+ * EAGLE-2 dynamic draft tree; "Medusa": candidates form a tree).  Candidate
+ * (w, v) of a request has the value
+ *     beam_scores[w] + l[w, v] - log sum_v' exp(l[w, v']);
+ * the K largest are kept, equal values in order of w V + v.
+ *   logits       [B, W, V] of `dtype`, row stride `row_stride` elements.  Rows
+ *                need no alignment beyond their element's.
+ *   beam_scores  [B, W] float32 cumulative log probabilities; -inf: the beam
+ *                holds no hypothesis and has no candidates (its row is not
+ *                read)
+ *   finished     [B, W] int32 or NULL; nonzero: a hypothesis that has ended.
+ *                Its one candidate is (w, eos_token) with the value
+ *                beam_scores[w]; its row is not read.  eos_token in [0, V) is
+ *                checked when finished is given.
+ *   out_scores   [B, K] float32, descending; out_parents, out_tokens [B, K]
+ *                int32: the beam w and the token v of each
+ * A logit of -inf is no candidate; with fewer than K candidates the rest is
+ * (-inf, -1, -1).  A request with a score of NaN or +inf, or with a NaN or
+ * +inf logit in a row that is read, gets scores NaN, parents and tokens -1.
+ * The row sums are taken in fp32 per vector and fp64 beyond, values are
+ * compared in fp64 and rounded once: scores are within 2^-24 relative plus
+ * 4e-6 absolute of the definition, and candidates whose values differ by more
+ * than 8e-6 are in the definition's order (candidates of one beam always are).
+ * Limits: 1 <= W, K <= SPECDEC_MAX_BEAMS.  Workspace:
+ * specdec_workspace_size_beam; its contents need no initialisation for this
+ * call, and the words other calls need zero stay as they are. */
+size_t specdec_workspace_size_beam(int B, int W, int K, int V, specdec_dtype dtype);
+specdec_status specdec_beam_select(const void* logits, specdec_dtype dtype, int64_t row_stride,
+                                   const float* beam_scores, const int32_t* finished, int eos_token, int B, int W,
+                                   int K, int V, float* out_scores, int32_t* out_parents, int32_t* out_tokens,
+                                   void* ws, size_t ws_bytes, struct CUstream_st* stream);
+
+/* Reordering of beam states after a selection: in every group (a layer's keys
+ * or values) and head, row (b, i) becomes row (b, parents[b, i]) over the
+ * positions below lengths[b].
+ *   src, dst     byte addresses of [G, B, W, H, T] rows of row_bytes bytes;
+ *                strides in BYTES in that order (G, B, W, H, T).  dst == src
+ *                (equal strides) reorders in place; otherwise the two must
+ *                not overlap.
+ *   parents      [B, W] int32; a row whose parent is outside [0, W) is left as
+ *                it is (not written)
+ *   lengths      [B] int32 (clamped to [0, T]) or NULL for T; positions from
+ *                lengths[b] on are neither read nor written
+ * Any address and size is served; accesses are as wide as addresses, strides
+ * and row_bytes allow (16 bytes for the best speed). */
+specdec_status specdec_reorder_states(const void* src, void* dst, const int32_t* parents, const int32_t* lengths,
+                                      int64_t G, int B, int W, int64_t H, int64_t T, int64_t row_bytes,
+                                      const int64_t src_strides[5], const int64_t dst_strides[5],
+                                      struct CUstream_st* stream);
+
+/* Block tables and slot maps of a paged cache for the rows the next verify
+ * step scores.  Position p of request b lies in slot
+ * block_tables[b, p / block_size] * block_size + p % block_size.
+ *   seq_lens     [B] int32 positions in the cache
+ *   accept_len   [B] int32 of the last verify step, or NULL: a request with
+ *                h >= 0 moves on by h + 1 positions (the token before the
+ *                drafts and the accepted drafts), one with -1 stays
+ *   release      [B] int32 or NULL; nonzero: the request has ended.  Its pages
+ *                go back to the ring, its length and held pages become 0, its
+ *                rows get position and slot -1
+ *   rows         k + 1 per request (k drafts, or the N nodes of a tree), or
+ *                with draft_offsets ([B + 1], packed layout, every k_b <= k)
+ *                those of the packed verifiers: row off[b] + b + j.  A request
+ *                with invalid offsets gets no pages and no rows are written.
+ *   block_tables [B, max_blocks] int32, row stride table_stride; entries
+ *                [held, new held) are written
+ *   held_blocks  [B] int32 pages of each table (clamped to [0, max_blocks])
+ *   free_ring    [ring_capacity] int32 free page numbers, ring_state [2] int32
+ *                = (head, count): entries head .. head + count - 1, modulo the
+ *                capacity.  The capacity must be at least the number of pages
+ *                (held and free).  Pages are taken from the head in request
+ *                order and returned behind the tail in request order.
+ *   seq_lens_out, held_out, ring_state_out: the new values; each may be the
+ *                array it replaces
+ *   positions, slots [rows] int64: len_b + j and its slot
+ * A request gets all the pages it asks for when the requests up to and
+ * including it ask for no more than the ring holds (pages returned in this
+ * call are not granted in it) and its table has room; otherwise none.  A row
+ * without a page gets slot -1 (its position is still written). */
+specdec_status specdec_plan_slots(const int32_t* seq_lens, const int32_t* accept_len, const int32_t* release,
+                                  const int32_t* draft_offsets, int B, int k, int64_t total_drafts, int block_size,
+                                  int32_t* block_tables, int64_t table_stride, int max_blocks,
+                                  const int32_t* held_blocks, int32_t* free_ring, int ring_capacity,
+                                  const int32_t* ring_state, int32_t* seq_lens_out, int32_t* held_out,
+                                  int32_t* ring_state_out, int64_t* positions, int64_t* slots,
+                                  struct CUstream_st* stream);
+
+/* The states of an accepted tree path (specdec_verify_tree) to the slots of
+ * the request's next positions: for j = 0 .. accept_len[b], the row of node 0
+ * (j = 0) or accept_nodes[b, j - 1] goes to row dst_slots[b, j] of the cache,
+ * in every group.  Strides in BYTES.
+ *   src          [G, B, N + 1] rows of row_bytes bytes, or with src_slots
+ *                ([B, N + 1] int64) rows of a cache [G, src_rows] named by the
+ *                node's slot
+ *   dst          [G, dst_rows] rows; dst_slots [B, >= max_depth + 1] int64
+ *   accept_len   [B], accept_nodes [B, max_depth] int32 as the tree call
+ *                returns them; accept_len -1 moves nothing
+ * A node outside [0, N] or a slot outside its cache moves nothing.  src and
+ * dst must not overlap, except that both may be one cache with src_slots ==
+ * dst_slots in content (node c was scored in the slot of position len + c):
+ * the path is then moved in place.  Slots of different requests must differ. */
+specdec_status specdec_commit_path(const void* src, int64_t src_group_stride, int64_t src_request_stride,
+                                   int64_t src_row_stride, const int64_t* src_slots, int64_t src_slots_stride,
+                                   int64_t src_rows, void* dst, int64_t dst_group_stride, int64_t dst_row_stride,
+                                   const int64_t* dst_slots, int64_t dst_slots_stride, int64_t dst_rows,
+                                   const int32_t* accept_len, const int32_t* accept_nodes, int64_t G, int B, int N,
+                                   int max_depth, int64_t row_bytes, struct CUstream_st* stream);
 
 /* Greedy verification without a caller workspace.  The pages have no
  * counterpart: this entry point exists for callers that cannot allocate

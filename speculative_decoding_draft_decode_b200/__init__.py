@@ -29,7 +29,8 @@ __all__ = [
     "SPECDEC_MODE_TREE", "SpecdecError", "lib", "library_path", "header_path",
     "specdec_workspace_size", "specdec_workspace_init", "specdec_verify_greedy",
     "specdec_verify_rejection", "specdec_verify_rejection_slice", "specdec_verify_tree", "specdec_status_string", "specdec_abi_version",
-    "Verifier",
+    "Verifier", "specdec_workspace_size_beam", "specdec_beam_select", "specdec_reorder_states", "specdec_commit_path",
+    "specdec_plan_slots", "reorder_states", "commit_path", "plan_slots",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -56,6 +57,8 @@ MAX_K = 32
 MAX_TOPK = 8
 MAX_DEPTH = 32
 MAX_TREE_NODES = 1024
+MAX_BEAMS = 32
+MAX_PLAN_ROWS = 1 << 24
 
 
 class SpecdecError(RuntimeError):
@@ -126,6 +129,17 @@ def lib():
         for f in ("specdec_shard_rejection_rows", "specdec_shard_rejection_decide", "specdec_shard_rejection_masses",
                   "specdec_shard_rejection_sample", "specdec_shard_rejection_finish"):
             getattr(L, f).restype = i32
+        L.specdec_workspace_size_beam.argtypes = [i32, i32, i32, i32, i32]
+        L.specdec_workspace_size_beam.restype = sz
+        L.specdec_beam_select.argtypes = [P, i32, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P, sz, P]
+        L.specdec_beam_select.restype = i32
+        L.specdec_reorder_states.argtypes = [P, P, P, P, i64, i32, i32, i64, i64, i64, P, P, P]
+        L.specdec_reorder_states.restype = i32
+        L.specdec_commit_path.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, i64, P, i64, i64, P, P, i64, i32, i32,
+                                          i32, i64, P]
+        L.specdec_commit_path.restype = i32
+        L.specdec_plan_slots.argtypes = [P, P, P, P, i32, i32, i64, i32, P, i64, i32, P, P, i32, P, P, P, P, P, P, P]
+        L.specdec_plan_slots.restype = i32
         L.specdec_set_prefetch_inputs.argtypes = [i32]
         L.specdec_set_prefetch_inputs.restype = i32
         L.specdec_tier_update.argtypes = [P, ctypes.c_double, ctypes.c_double]
@@ -318,6 +332,232 @@ def ngram_propose(tokens, lengths, n_min: int = 2, n_max: int = 5, k: int = 4, p
     return (d[:, :k], n, off, packed) if pack else (d[:, :k], n)
 
 
+def specdec_workspace_size_beam(B: int, W: int, K: int, V: int, dtype: int) -> int:
+    return lib().specdec_workspace_size_beam(B, W, K, V, dtype)
+
+
+def specdec_beam_select(logits, dtype, row_stride, beam_scores, finished, eos_token, B, W, K, V, out_scores,
+                        out_parents, out_tokens, ws, ws_bytes, stream=None) -> int:
+    return lib().specdec_beam_select(_ptr(logits), dtype, row_stride, _ptr(beam_scores), _ptr(finished), eos_token, B,
+                                     W, K, V, _ptr(out_scores), _ptr(out_parents), _ptr(out_tokens), _ptr(ws),
+                                     ws_bytes, _stream(stream))
+
+
+def specdec_reorder_states(src, dst, parents, lengths, G, B, W, H, T, row_bytes, src_strides, dst_strides,
+                           stream=None) -> int:
+    """src_strides, dst_strides: five byte strides each (groups, requests, beams, heads, positions)."""
+    five = ctypes.c_int64 * 5
+    return lib().specdec_reorder_states(_ptr(src), _ptr(dst), _ptr(parents), _ptr(lengths), G, B, W, H, T, row_bytes,
+                                        five(*src_strides), five(*dst_strides), _stream(stream))
+
+
+def specdec_commit_path(src, src_group_stride, src_request_stride, src_row_stride, src_slots, src_slots_stride,
+                        src_rows, dst, dst_group_stride, dst_row_stride, dst_slots, dst_slots_stride, dst_rows,
+                        accept_len, accept_nodes, G, B, N, max_depth, row_bytes, stream=None) -> int:
+    return lib().specdec_commit_path(_ptr(src), src_group_stride, src_request_stride, src_row_stride, _ptr(src_slots),
+                                     src_slots_stride, src_rows, _ptr(dst), dst_group_stride, dst_row_stride,
+                                     _ptr(dst_slots), dst_slots_stride, dst_rows, _ptr(accept_len),
+                                     _ptr(accept_nodes), G, B, N, max_depth, row_bytes, _stream(stream))
+
+
+def specdec_plan_slots(seq_lens, accept_len, release, draft_offsets, B, k, total_drafts, block_size, block_tables,
+                       table_stride, max_blocks, held_blocks, free_ring, ring_capacity, ring_state, seq_lens_out,
+                       held_out, ring_state_out, positions, slots, stream=None) -> int:
+    return lib().specdec_plan_slots(_ptr(seq_lens), _ptr(accept_len), _ptr(release), _ptr(draft_offsets), B, k,
+                                    total_drafts, block_size, _ptr(block_tables), table_stride, max_blocks,
+                                    _ptr(held_blocks), _ptr(free_ring), ring_capacity, _ptr(ring_state),
+                                    _ptr(seq_lens_out), _ptr(held_out), _ptr(ring_state_out), _ptr(positions),
+                                    _ptr(slots), _stream(stream))
+
+
+# ---------------------------------------------------------------------------
+# The caches around a verify step (torch layer)
+# ---------------------------------------------------------------------------
+def _typed(t, dtype, shape, name):
+    """t, checked to be a contiguous tensor of that type and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, list(shape)))
+    return t
+
+
+def _span(t):
+    """First and last byte + 1 of the memory a tensor's elements lie in."""
+    n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
+    at = t.data_ptr()
+    return at, at + n * t.element_size()
+
+
+def _overlap(a, b):
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _row_elems(t, dims, name):
+    """Elements of a row: the dimensions from `dims` on, which must lie one behind the other."""
+    n = 1
+    for d in range(t.dim() - 1, dims - 1, -1):
+        if t.shape[d] != 1 and t.stride(d) != n:
+            raise ValueError("%s: the dimensions of a row must be contiguous" % name)
+        n *= t.shape[d]
+    return n
+
+
+def _used_on(stream, *tensors):
+    """Fresh outputs written on another stream than the one they were
+    allocated on: their memory is not handed out again before it is done."""
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def reorder_states(states, parents, lengths=None, time_dim: int = 3, stream=None, out=None):
+    """Row (b, i) of every group becomes row (b, parents[b, i]) over the
+    positions below lengths[b] (all of them without lengths), after a beam
+    selection.  states [G, B, W, T, ...] (time_dim 3) or [G, B, W, H, T, ...]
+    (time_dim 4): G groups such as layers' keys and values, what follows the
+    position a contiguous row.  parents int32 [B, W]; a row whose parent is
+    outside [0, W) is left as it is.  In place, or into `out` (same shape and
+    type, no overlap).  Returns what was written."""
+    import torch
+    to = states if out is None else out
+    if time_dim not in (3, 4) or states.dim() <= time_dim:
+        raise ValueError("states must be [G, B, W, T, ...] (time_dim 3) or [G, B, W, H, T, ...] (time_dim 4)")
+    if to.shape != states.shape or to.dtype != states.dtype:
+        raise ValueError("out must have the shape and type of states")
+    _on_current_device(states, to, parents, lengths, stream=stream)
+    shape = states.shape
+    G, B, W, T = shape[0], shape[1], shape[2], shape[time_dim]
+    H = shape[3] if time_dim == 4 else 1
+    _typed(parents, torch.int32, (B, W), "parents")
+    if lengths is not None:
+        _typed(lengths, torch.int32, (B,), "lengths")
+    es = states.element_size()
+    row = _row_elems(states, time_dim + 1, "states") * es
+    if to.numel() == 0:
+        return to
+    strides = [s * es for s in states.stride()[:time_dim + 1]]
+    if to is states or (to.data_ptr() == states.data_ptr() and to.stride() == states.stride()):
+        dst_strides = strides
+    else:
+        _row_elems(to, time_dim + 1, "out")
+        dst_strides = [s * es for s in to.stride()[:time_dim + 1]]
+        if _overlap(states, to):
+            raise ValueError("out overlaps states: pass none to reorder in place")
+    if any(s < row and n > 1 for s, n in zip(dst_strides, shape)):
+        raise ValueError("the rows written must not share memory")
+    if time_dim == 3:
+        strides = [*strides[:3], 0, strides[3]]
+        dst_strides = [*dst_strides[:3], 0, dst_strides[3]]
+    _check(specdec_reorder_states(states, to, parents, lengths, G, B, W, H, T, row, strides, dst_strides, stream),
+           "reorder_states")
+    return to
+
+
+def commit_path(src, accept_len, accept_nodes, dst, dst_slots, src_slots=None, stream=None):
+    """The states of the accepted tree paths into the cache: row accept_nodes
+    [b, j - 1] of request b (node 0, the root, for j = 0) goes to slot
+    dst_slots[b, j] for j = 0 .. accept_len[b].  src [G, B, N + 1, ...] (the
+    tree's own states), or with src_slots (int64 [B, N + 1]) a cache [G, S,
+    ...]; dst [G, slots, ...]; dst_slots int64 [B, >= max_depth + 1] (for the
+    slots of plan_slots with k = N: slots.view(B, N + 1)).  src and dst may be
+    one cache when src_slots and dst_slots hold the same slots.  Returns dst."""
+    import torch
+    _on_current_device(src, accept_len, accept_nodes, dst, dst_slots, src_slots, stream=stream)
+    if accept_nodes.dim() != 2:
+        raise ValueError("accept_nodes must be [B, max_depth]")
+    B, depth = accept_nodes.shape
+    _typed(accept_nodes, torch.int32, (B, depth), "accept_nodes")
+    _typed(accept_len, torch.int32, (B,), "accept_len")
+    lead = 3 if src_slots is None else 2
+    if src.dim() < lead or dst.dim() < 2 or src.dtype != dst.dtype or src.shape[lead:] != dst.shape[2:] \
+            or src.shape[0] != dst.shape[0]:
+        raise ValueError("src must be [G, B, N + 1, ...] (with src_slots [G, S, ...]) and dst [G, slots, ...] of its type")
+    for name, t in (("dst_slots", dst_slots), ("src_slots", src_slots)):
+        if t is not None and (t.dtype != torch.int64 or t.dim() != 2 or t.shape[0] != B or t.stride(1) != 1
+                              or (B > 1 and t.stride(0) < t.shape[1])):
+            raise ValueError("%s must be an int64 [B, n] tensor with contiguous rows" % name)
+    if dst_slots.shape[1] < depth + 1:
+        raise ValueError("dst_slots must have max_depth + 1 columns at least")
+    es = src.element_size()
+    row = _row_elems(src, lead, "src") * es
+    _row_elems(dst, 2, "dst")
+    if src.numel() == 0 or dst.numel() == 0 or B == 0:
+        return dst
+    if src_slots is None:
+        if src.shape[1] != B:
+            raise ValueError("src must be [G, B, N + 1, ...]")
+        nodes, src_rows, ss = src.shape[2], 0, 0
+        sg, sb, sr = (s * es for s in src.stride()[:3])
+        sr = max(sr, row) if nodes == 1 else sr
+    else:
+        nodes, src_rows, ss = src_slots.shape[1], src.shape[1], max(src_slots.stride(0), src_slots.shape[1])
+        sg, sr = (s * es for s in src.stride()[:2])
+        sr = max(sr, row) if src_rows == 1 else sr
+        sb = 0
+    dg, dr = (s * es for s in dst.stride()[:2])
+    dr = max(dr, row) if dst.shape[1] == 1 else dr
+    same = src_slots is not None and src.data_ptr() == dst.data_ptr() and src.stride() == dst.stride()
+    if not same and _overlap(src, dst):
+        raise ValueError("src and dst overlap: in place both must be the same cache, with src_slots")
+    if dst.shape[0] > 1 and dg < row:
+        raise ValueError("the rows written must not share memory")
+    _check(specdec_commit_path(src, sg, sb, sr, src_slots, ss, src_rows, dst, dg, dr, dst_slots,
+                               max(dst_slots.stride(0), dst_slots.shape[1]), dst.shape[1], accept_len, accept_nodes,
+                               src.shape[0], B, nodes - 1, depth, row, stream), "commit_path")
+    return dst
+
+
+def plan_slots(seq_lens, block_tables, held_blocks, free_ring, ring_state, block_size: int, k: int = 0,
+               draft_offsets=None, total_drafts: int = 0, accept_len=None, release=None, stream=None, out=None):
+    """Cache slots for the rows the next verify step scores: k + 1 per request,
+    or those of the packed layout with draft_offsets [B + 1] (then k bounds
+    every request's drafts).  seq_lens, held_blocks, accept_len, release int32
+    [B]; block_tables int32 [B, max_blocks] and free_ring int32 are updated in
+    place; ring_state int32 [2] (head, count).  Returns (seq_lens, held_blocks,
+    ring_state, positions int64 [rows], slots int64 [rows]): the new values,
+    in `out` when given (whose first three may be the arrays they replace)."""
+    import torch
+    B = seq_lens.numel()
+    _on_current_device(seq_lens, block_tables, held_blocks, free_ring, ring_state, draft_offsets, accept_len, release,
+                       *(out or ()), stream=stream)
+    i32 = torch.int32
+    _typed(seq_lens, i32, (B,), "seq_lens")
+    _typed(held_blocks, i32, (B,), "held_blocks")
+    if accept_len is not None:
+        _typed(accept_len, i32, (B,), "accept_len")
+    if release is not None:
+        _typed(release, i32, (B,), "release")
+    _typed(free_ring, i32, (free_ring.numel(),), "free_ring")
+    _typed(ring_state, i32, (2,), "ring_state")
+    if block_tables.dtype != i32 or block_tables.dim() != 2 or block_tables.shape[0] != B \
+            or block_tables.stride(1) != 1 or (B > 1 and block_tables.stride(0) < block_tables.shape[1]):
+        raise ValueError("block_tables must be an int32 [B, max_blocks] tensor with contiguous rows")
+    if draft_offsets is not None:
+        _typed(draft_offsets, i32, (B + 1,), "draft_offsets")
+        rows = B + total_drafts
+    else:
+        rows = B * (k + 1)
+    if rows < 0:
+        raise ValueError("k and total_drafts must not be negative")
+    if out is None:
+        dev = seq_lens.device
+        out = (torch.empty(B, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
+               ring_state.clone() if B == 0 else torch.empty(2, dtype=i32, device=dev),
+               torch.empty(rows, dtype=torch.int64, device=dev), torch.empty(rows, dtype=torch.int64, device=dev))
+        _used_on(stream, *out)
+    else:
+        for t, dt, n, name in zip(out, (i32, i32, i32, torch.int64, torch.int64), (B, B, 2, rows, rows),
+                                  ("seq_lens", "held_blocks", "ring_state", "positions", "slots")):
+            _typed(t, dt, (n,), "out: " + name)
+    cols = block_tables.shape[1]
+    lens, held, state, positions, slots = out
+    _check(specdec_plan_slots(seq_lens, accept_len, release, draft_offsets, B, k, total_drafts, block_size,
+                              block_tables, block_tables.stride(0) if B > 1 else cols, cols, held_blocks, free_ring,
+                              free_ring.numel(), ring_state, lens, held, state, positions, slots, stream),
+           "plan_slots")
+    return lens, held, state, positions, slots
+
+
 def specdec_set_prefetch_inputs(enable: bool) -> bool:
     """Process-wide: let the streaming pass read its logit rows before the
     previous kernel of the stream has finished (see the header for when that
@@ -389,6 +629,7 @@ class Verifier:
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self._ws = None
         self._ws_bytes = 0
+        self._outgrown = []  # smaller workspaces: captured graphs and other streams may still use them
 
     def _on_device(self, *tensors):
         """Every tensor argument must live on this verifier's CUDA device (any
@@ -408,6 +649,8 @@ class Verifier:
             nbytes = max(nbytes, 2 * self._ws_bytes)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             _check(specdec_workspace_init(ws, nbytes, stream), "workspace_init")
+            if self._ws is not None:
+                self._outgrown.append(self._ws)
             self._ws, self._ws_bytes = ws, nbytes
         return self._ws, self._ws_bytes
 
@@ -436,6 +679,38 @@ class Verifier:
         _check(specdec_verify_greedy(logits, dt, stride, d if k > 0 else None, B, k, V, al, ot, topk, ids, vals,
                                      ws, wsb, stream), "verify_greedy")
         return (al, ot, ids, vals) if topk else (al, ot)
+
+    def beam_select(self, logits, beam_scores, num_beams: int, finished=None, eos_token: int = 0, stream=None,
+                    out=None):
+        """One step of beam search, or one level of a draft tree: logits
+        [B, W, V] (bf16/f32), beam_scores float32 [B, W] (cumulative log
+        probabilities, -inf: no hypothesis), finished int32 [B, W] or None ->
+        (scores float32 [B, num_beams], parents, tokens int32 [B, num_beams]),
+        the best continuations in descending order."""
+        import torch
+        _on_current_device(logits, beam_scores, finished, *(out or ()), stream=stream)
+        self._on_device(logits)
+        dt = _dtype_code(logits)
+        stride = _row_stride(logits, "logits")
+        B, W, V = logits.shape
+        K = num_beams
+        _typed(beam_scores, torch.float32, (B, W), "beam_scores")
+        if finished is not None:
+            _typed(finished, torch.int32, (B, W), "finished")
+        if out is None:
+            dev = logits.device
+            out = (torch.empty(B, max(K, 0), dtype=torch.float32, device=dev),
+                   torch.empty(B, max(K, 0), dtype=torch.int32, device=dev),
+                   torch.empty(B, max(K, 0), dtype=torch.int32, device=dev))
+            _used_on(stream, *out)
+        else:
+            for t, d, name in zip(out, (torch.float32, torch.int32, torch.int32), ("scores", "parents", "tokens")):
+                _typed(t, d, (B, K), "out: " + name)
+        scores, parents, tokens = out
+        ws, wsb = self.workspace(specdec_workspace_size_beam(B, W, K, V, dt), stream)
+        _check(specdec_beam_select(logits, dt, stride, beam_scores, finished, eos_token, B, W, K, V, scores, parents,
+                                   tokens, ws, wsb, stream), "beam_select")
+        return scores, parents, tokens
 
     def tree(self, logits, parents, node_tokens, max_depth: int, stream=None, out=None):
         """logits [B, N+1, V], parents/node_tokens [B, N+1] int32 ->

@@ -20,6 +20,9 @@
 #include "verify_resample.cuh"
 #include "verify_stats.cuh"
 #include "verify_ngram.cuh"
+#include "beam_select.cuh"
+#include "slots.cuh"
+#include "states.cuh"
 
 namespace specdec {
 namespace {
@@ -211,6 +214,71 @@ void fill_common(Pass1Params& P, const void* logits, int64_t row_stride, int V, 
 
 namespace specdec {
 namespace {
+
+// Beam selection: the chunks' statistics and best keys, behind the fixed area
+// (which it does not touch).
+struct BeamLayout {
+    int cpr = 0;
+    size_t stats = 0, keys = 0, total = 0;
+};
+
+BeamLayout make_beam_layout(int B, int W, int K, int V, specdec_dtype dtype) {
+    BeamLayout L;
+    const int ve = vec_elems(dtype);
+    L.cpr = static_cast<int>(chunks_per_row(V / ve, ve));
+    const size_t chunks = static_cast<size_t>(B) * static_cast<size_t>(W) * static_cast<size_t>(L.cpr);
+    L.stats = kPartialBase;
+    L.keys = align_up(L.stats + chunks * sizeof(BeamStat), 256);
+    L.total = align_up(L.keys + chunks * static_cast<size_t>(K) * sizeof(uint64_t), 256);
+    return L;
+}
+
+template <class Tag>
+specdec_status launch_beam(const BeamParams& P, cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(P.B) * P.W;
+    if (P.cpr > 65535) return SPECDEC_ERR_UNSUPPORTED;  // grid limit
+    const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(P.cpr));
+    if (launch_pdl(beam_pass_kernel<Tag, Tag::VEC>, grid, 0, stream, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
+    if (launch_pdl(beam_merge_kernel, dim3(static_cast<unsigned>(P.B)), 0, stream, P) != cudaSuccess)
+        return SPECDEC_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+// CTAs of a copy kernel: enough to fill the GPU several times over, each
+// taking the next work item in turn.
+unsigned copy_grid(int64_t items) {
+    constexpr int64_t kMost = 148 * 16;
+    return static_cast<unsigned>(items < kMost ? items : kMost);
+}
+
+template <class VT, int WT, int C>
+specdec_status launch_reorder_as(ReorderParams P, cudaStream_t stream) {
+    P.tiles = (P.T * P.row + NT * C - 1) / (NT * C);
+    const int64_t items = P.G * P.H * P.B * P.tiles;
+    if (launch_pdl(reorder_states_kernel<VT, WT, C>, dim3(copy_grid(items)), 0, stream, P) != cudaSuccess)
+        return SPECDEC_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+template <class VT>
+specdec_status launch_reorder(ReorderParams P, int64_t row_bytes, cudaStream_t stream) {
+    P.row = row_bytes / static_cast<int64_t>(sizeof(VT));
+    if (P.W <= 2) return launch_reorder_as<VT, 2, 8>(P, stream);
+    if (P.W <= 4) return launch_reorder_as<VT, 4, 4>(P, stream);
+    if (P.W <= 8) return launch_reorder_as<VT, 8, 2>(P, stream);
+    if (P.W <= 16) return launch_reorder_as<VT, 16, 1>(P, stream);
+    return launch_reorder_as<VT, 32, 1>(P, stream);
+}
+
+template <class VT>
+specdec_status launch_commit(CommitParams P, int64_t row_bytes, cudaStream_t stream) {
+    P.row = row_bytes / static_cast<int64_t>(sizeof(VT));
+    P.tiles = (P.row + NT - 1) / NT;
+    const int64_t items = P.G * P.B * P.tiles;
+    if (launch_pdl(commit_path_kernel<VT>, dim3(copy_grid(items)), 0, stream, P) != cudaSuccess)
+        return SPECDEC_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
 
 // Every check specdec_verify_greedy makes before it launches anything, the
 // workspace's aside (B == 0 passes: such a call does nothing).
@@ -913,6 +981,209 @@ specdec_status specdec_ngram_propose(const int32_t* tokens, int64_t token_stride
     if (launch_pdl(verify_ngram_kernel, dim3(static_cast<unsigned>(B)), 0, s, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
     if (draft_offsets != nullptr && launch_pdl(verify_ngram_pack_kernel, dim3(1), 0, s, P) != cudaSuccess)
         return SPECDEC_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+size_t specdec_workspace_size_beam(int B, int W, int K, int V, specdec_dtype dtype) {
+    if (!dtype_ok(dtype) || B < 0 || B > SPECDEC_MAX_B || W < 1 || W > SPECDEC_MAX_BEAMS || K < 1 ||
+        K > SPECDEC_MAX_BEAMS || V < 1 || V > SPECDEC_MAX_V)
+        return 0;
+    return make_beam_layout(B, W, K, V, dtype).total;
+}
+
+specdec_status specdec_beam_select(const void* logits, specdec_dtype dtype, int64_t row_stride,
+                                   const float* beam_scores, const int32_t* finished, int eos_token, int B, int W,
+                                   int K, int V, float* out_scores, int32_t* out_parents, int32_t* out_tokens,
+                                   void* ws, size_t ws_bytes, struct CUstream_st* stream) {
+    if (!dtype_ok(dtype)) return SPECDEC_ERR_UNSUPPORTED;
+    if (B < 0 || B > SPECDEC_MAX_B || W < 1 || W > SPECDEC_MAX_BEAMS || K < 1 || K > SPECDEC_MAX_BEAMS || V < 1 ||
+        V > SPECDEC_MAX_V)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (finished != nullptr && (eos_token < 0 || eos_token >= V)) return SPECDEC_ERR_INVALID_ARG;
+    if (B == 0) return SPECDEC_OK;
+    const int64_t rows = static_cast<int64_t>(B) * W;
+    if (!rows_fit(rows, row_stride, V)) return SPECDEC_ERR_INVALID_ARG;
+    if (logits == nullptr || beam_scores == nullptr || out_scores == nullptr || out_parents == nullptr ||
+        out_tokens == nullptr)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % static_cast<uintptr_t>(elem_size(dtype)) != 0)
+        return SPECDEC_ERR_INVALID_ARG;
+    const BeamLayout L = make_beam_layout(B, W, K, V, dtype);
+    specdec_status st = check_ws(ws, ws_bytes, L.total);
+    if (st != SPECDEC_OK) return st;
+    BeamParams P;
+    P.logits = logits;
+    P.row_stride = row_stride;
+    P.scores = beam_scores;
+    P.finished = finished;
+    P.B = B;
+    P.W = W;
+    P.K = K;
+    P.V = V;
+    P.eos = eos_token;
+    P.cpr = L.cpr;
+    P.stats = reinterpret_cast<BeamStat*>(static_cast<char*>(ws) + L.stats);
+    P.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + L.keys);
+    P.out_scores = out_scores;
+    P.out_parents = out_parents;
+    P.out_tokens = out_tokens;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == SPECDEC_BF16 ? launch_beam<BF16Tag>(P, s) : launch_beam<F32Tag>(P, s);
+}
+
+specdec_status specdec_reorder_states(const void* src, void* dst, const int32_t* parents, const int32_t* lengths,
+                                      int64_t G, int B, int W, int64_t H, int64_t T, int64_t row_bytes,
+                                      const int64_t src_strides[5], const int64_t dst_strides[5],
+                                      struct CUstream_st* stream) {
+    if (B < 0 || B > SPECDEC_MAX_B || W < 1 || W > SPECDEC_MAX_BEAMS || G < 0 || H < 0 || T < 0 || row_bytes < 0)
+        return SPECDEC_ERR_INVALID_ARG;
+    constexpr int64_t kMost = int64_t(1) << 40;
+    if (G > kMost || H > kMost || T > kMost || row_bytes > kMost) return SPECDEC_ERR_INVALID_ARG;
+    if (src_strides == nullptr || dst_strides == nullptr) return SPECDEC_ERR_INVALID_ARG;
+    if (B == 0 || G == 0 || H == 0 || T == 0 || row_bytes == 0) return SPECDEC_OK;
+    // Bytes of one beam of everything: every index below stays in 63 bits.
+    if (static_cast<double>(G) * static_cast<double>(H) * B *
+            (static_cast<double>(T) * static_cast<double>(row_bytes) + 65536.0) > 0x1p60)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (src == nullptr || dst == nullptr || parents == nullptr) return SPECDEC_ERR_INVALID_ARG;
+    for (int i = 0; i < 5; ++i)
+        if (src_strides[i] < 0 || dst_strides[i] < 0 || src_strides[i] > (int64_t(1) << 52) ||
+            dst_strides[i] > (int64_t(1) << 52) || (src == dst && src_strides[i] != dst_strides[i]))
+            return SPECDEC_ERR_INVALID_ARG;
+    ReorderParams P;
+    P.src = static_cast<const char*>(src);
+    P.dst = static_cast<char*>(dst);
+    P.parents = parents;
+    P.lengths = lengths;
+    P.G = G;
+    P.H = H;
+    P.B = B;
+    P.W = W;
+    P.T = T;
+    P.sg = src_strides[0];
+    P.sb = src_strides[1];
+    P.sw = src_strides[2];
+    P.sh = src_strides[3];
+    P.st = src_strides[4];
+    P.dg = dst_strides[0];
+    P.db = dst_strides[1];
+    P.dw = dst_strides[2];
+    P.dh = dst_strides[3];
+    P.dt = dst_strides[4];
+    P.flat = (T == 1 || (P.st == row_bytes && P.dt == row_bytes)) ? 1 : 0;
+    P.in_place = src == dst ? 1 : 0;
+    // The widest access that every address allows.
+    uint64_t bits = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
+                    static_cast<uint64_t>(row_bytes);
+    const int64_t dims[5] = {G, B, W, H, T};
+    for (int i = 0; i < 5; ++i)
+        if (dims[i] > 1) bits |= static_cast<uint64_t>(src_strides[i]) | static_cast<uint64_t>(dst_strides[i]);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (bits % 16 == 0) return launch_reorder<uint4>(P, row_bytes, s);
+    if (bits % 8 == 0) return launch_reorder<uint2>(P, row_bytes, s);
+    if (bits % 4 == 0) return launch_reorder<uint32_t>(P, row_bytes, s);
+    if (bits % 2 == 0) return launch_reorder<uint16_t>(P, row_bytes, s);
+    return launch_reorder<uint8_t>(P, row_bytes, s);
+}
+
+specdec_status specdec_commit_path(const void* src, int64_t src_group_stride, int64_t src_request_stride,
+                                   int64_t src_row_stride, const int64_t* src_slots, int64_t src_slots_stride,
+                                   int64_t src_rows, void* dst, int64_t dst_group_stride, int64_t dst_row_stride,
+                                   const int64_t* dst_slots, int64_t dst_slots_stride, int64_t dst_rows,
+                                   const int32_t* accept_len, const int32_t* accept_nodes, int64_t G, int B, int N,
+                                   int max_depth, int64_t row_bytes, struct CUstream_st* stream) {
+    if (B < 0 || B > SPECDEC_MAX_B || N < 0 || N + 1 > SPECDEC_MAX_TREE_NODES || max_depth < 1 ||
+        max_depth > SPECDEC_MAX_DEPTH || G < 0 || row_bytes < 0)
+        return SPECDEC_ERR_INVALID_ARG;
+    constexpr int64_t kMost = int64_t(1) << 40;
+    if (G > kMost || row_bytes > kMost || src_rows < 0 || dst_rows < 0 || src_rows > kMost || dst_rows > kMost)
+        return SPECDEC_ERR_INVALID_ARG;
+    const int64_t strides[5] = {src_group_stride, src_request_stride, src_row_stride, dst_group_stride,
+                                dst_row_stride};
+    for (int i = 0; i < 5; ++i)
+        if (strides[i] < 0 || strides[i] > kMost) return SPECDEC_ERR_INVALID_ARG;
+    if (B == 0 || G == 0 || row_bytes == 0) return SPECDEC_OK;
+    if (static_cast<double>(G) * B * (static_cast<double>(row_bytes) + 65536.0) > 0x1p60)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (src == nullptr || dst == nullptr || dst_slots == nullptr || accept_len == nullptr || accept_nodes == nullptr)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (dst_slots_stride < max_depth + 1 || (src_slots != nullptr && src_slots_stride < N + 1))
+        return SPECDEC_ERR_INVALID_ARG;
+    if (src_row_stride < row_bytes || dst_row_stride < row_bytes) return SPECDEC_ERR_INVALID_ARG;
+    CommitParams P;
+    P.src = static_cast<const char*>(src);
+    P.dst = static_cast<char*>(dst);
+    P.accept_len = accept_len;
+    P.accept_nodes = accept_nodes;
+    P.src_slots = src_slots;
+    P.dst_slots = dst_slots;
+    P.src_slots_stride = src_slots_stride;
+    P.dst_slots_stride = dst_slots_stride;
+    P.G = G;
+    P.B = B;
+    P.nodes = N + 1;
+    P.depth = max_depth;
+    P.src_rows = src_rows;
+    P.dst_rows = dst_rows;
+    P.sg = src_group_stride;
+    P.sb = src_slots != nullptr ? 0 : src_request_stride;
+    P.sr = src_row_stride;
+    P.dg = dst_group_stride;
+    P.dr = dst_row_stride;
+    const uint64_t bits = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
+                          static_cast<uint64_t>(row_bytes | P.sg | P.sb | P.sr | P.dg | P.dr);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (bits % 16 == 0) return launch_commit<uint4>(P, row_bytes, s);
+    if (bits % 8 == 0) return launch_commit<uint2>(P, row_bytes, s);
+    if (bits % 4 == 0) return launch_commit<uint32_t>(P, row_bytes, s);
+    if (bits % 2 == 0) return launch_commit<uint16_t>(P, row_bytes, s);
+    return launch_commit<uint8_t>(P, row_bytes, s);
+}
+
+specdec_status specdec_plan_slots(const int32_t* seq_lens, const int32_t* accept_len, const int32_t* release,
+                                  const int32_t* draft_offsets, int B, int k, int64_t total_drafts, int block_size,
+                                  int32_t* block_tables, int64_t table_stride, int max_blocks,
+                                  const int32_t* held_blocks, int32_t* free_ring, int ring_capacity,
+                                  const int32_t* ring_state, int32_t* seq_lens_out, int32_t* held_out,
+                                  int32_t* ring_state_out, int64_t* positions, int64_t* slots,
+                                  struct CUstream_st* stream) {
+    if (B < 0 || B > SPECDEC_MAX_B || k < 0 || k > SPECDEC_MAX_PLAN_ROWS - 1 || block_size < 1 ||
+        block_size > SPECDEC_MAX_PLAN_ROWS || max_blocks < 1 || table_stride < max_blocks ||
+        table_stride > (int64_t(1) << 40) || ring_capacity < 1)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (draft_offsets != nullptr && (total_drafts < 0 || total_drafts > static_cast<int64_t>(B) * k))
+        return SPECDEC_ERR_INVALID_ARG;
+    if (B == 0) return SPECDEC_OK;
+    if (seq_lens == nullptr || block_tables == nullptr || held_blocks == nullptr || free_ring == nullptr ||
+        ring_state == nullptr || seq_lens_out == nullptr || held_out == nullptr || ring_state_out == nullptr ||
+        positions == nullptr || slots == nullptr)
+        return SPECDEC_ERR_INVALID_ARG;
+    PlanParams P;
+    P.seq_lens = seq_lens;
+    P.accept_len = accept_len;
+    P.release = release;
+    P.offsets = draft_offsets;
+    P.B = B;
+    P.k = k;
+    P.total = draft_offsets != nullptr ? total_drafts : static_cast<int64_t>(B) * k;
+    P.block_size = block_size;
+    P.tables = block_tables;
+    P.table_stride = table_stride;
+    P.max_blocks = max_blocks;
+    P.held = held_blocks;
+    P.ring = free_ring;
+    P.capacity = ring_capacity;
+    P.ring_state = ring_state;
+    P.seq_out = seq_lens_out;
+    P.held_out = held_out;
+    P.ring_out = ring_state_out;
+    P.positions = positions;
+    P.slots = slots;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (launch_pdl(plan_tables_kernel, dim3(1), 0, s, P, kPlanThreads) != cudaSuccess) return SPECDEC_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>((B + NWARPS - 1) / NWARPS),
+                    static_cast<unsigned>(static_cast<int64_t>(k) / kSlotTile + 1));
+    if (launch_pdl(plan_slots_kernel, grid, 0, s, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 

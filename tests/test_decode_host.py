@@ -1,0 +1,153 @@
+"""Host-side checks of the operators around the verify step: every refusal
+comes before any CUDA call, so these run without a GPU."""
+import pytest
+import torch
+
+import speculative_decoding_draft_decode_b200 as sd
+from speculative_decoding_draft_decode_b200 import build as sd_build
+
+FAKE = 0x7F0000000000  # never dereferenced: every case below fails its checks first
+E, U, W, OK = sd.SPECDEC_ERR_INVALID_ARG, sd.SPECDEC_ERR_UNSUPPORTED, sd.SPECDEC_ERR_WORKSPACE, sd.SPECDEC_OK
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    sd_build.build()
+
+
+def beam(**kw):
+    a = dict(logits=FAKE, dtype=0, row_stride=1000, beam_scores=FAKE, finished=None, eos_token=0, B=4, W=4, K=4,
+             V=1000, out_scores=FAKE, out_parents=FAKE, out_tokens=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=0)
+    a.update(kw)
+    return sd.specdec_beam_select(**a)
+
+
+def test_beam_refusals():
+    assert beam(dtype=5) == U
+    for bad in (dict(B=-1), dict(B=sd.MAX_B + 1), dict(W=0), dict(W=33), dict(K=0), dict(K=33), dict(V=0),
+                dict(V=(1 << 24) + 1), dict(row_stride=999), dict(logits=None), dict(beam_scores=None),
+                dict(out_scores=None), dict(out_parents=None), dict(out_tokens=None), dict(logits=FAKE + 2),
+                dict(finished=FAKE, eos_token=1000), dict(finished=FAKE, eos_token=-1)):
+        assert beam(**bad) == E, bad
+    for bad in (dict(ws=None), dict(ws=FAKE + 4), dict(ws_bytes=1024)):
+        assert beam(**bad) == W, bad
+    assert beam(B=0, logits=None) == OK
+
+
+def test_beam_workspace_size():
+    f = sd.specdec_workspace_size_beam
+    assert f(64, 8, 8, 128256, sd.SPECDEC_BF16) > 65536 * 4
+    assert f(64, 8, 16, 128256, sd.SPECDEC_BF16) > f(64, 8, 8, 128256, sd.SPECDEC_BF16)
+    assert f(0, 8, 8, 1000, 0) >= 65536 * 4
+    for bad in ((-1, 4, 4, 100, 0), (4, 0, 4, 100, 0), (4, 33, 4, 100, 0), (4, 4, 0, 100, 0), (4, 4, 33, 100, 0),
+                (4, 4, 4, 0, 0), (4, 4, 4, 100, 2)):
+        assert f(*bad) == 0, bad
+    need = f(4, 4, 4, 1000, 0)
+    assert beam(ws_bytes=need - 1) == W
+
+
+def reorder(**kw):
+    a = dict(src=FAKE, dst=FAKE + (1 << 30), parents=FAKE, lengths=None, G=2, B=2, W=4, H=1, T=8, row_bytes=64,
+             src_strides=(4096, 2048, 512, 0, 64), dst_strides=(4096, 2048, 512, 0, 64), stream=0)
+    a.update(kw)
+    return sd.specdec_reorder_states(**a)
+
+
+def test_reorder_refusals():
+    for bad in (dict(B=-1), dict(B=sd.MAX_B + 1), dict(W=0), dict(W=33), dict(G=-1), dict(H=-1), dict(T=-1),
+                dict(row_bytes=-1), dict(src=None), dict(dst=None), dict(parents=None), dict(T=1 << 41),
+                dict(T=1 << 40, row_bytes=1 << 40), dict(src_strides=(-1, 2048, 512, 0, 64)),
+                dict(dst=FAKE, dst_strides=(4096, 2048, 512, 0, 128))):
+        assert reorder(**bad) == E, bad
+    for none in (dict(B=0), dict(G=0), dict(H=0), dict(T=0), dict(row_bytes=0)):
+        assert reorder(src=None, **none) == OK
+
+
+def commit(**kw):
+    a = dict(src=FAKE, src_group_stride=1 << 20, src_request_stride=1 << 12, src_row_stride=64, src_slots=None,
+             src_slots_stride=0, src_rows=0, dst=FAKE + (1 << 32), dst_group_stride=1 << 20, dst_row_stride=64,
+             dst_slots=FAKE, dst_slots_stride=7, dst_rows=100, accept_len=FAKE, accept_nodes=FAKE, G=2, B=2, N=10,
+             max_depth=6, row_bytes=64, stream=0)
+    a.update(kw)
+    return sd.specdec_commit_path(**a)
+
+
+def test_commit_refusals():
+    for bad in (dict(B=-1), dict(N=-1), dict(N=1024), dict(max_depth=0), dict(max_depth=33), dict(G=-1),
+                dict(row_bytes=-1), dict(dst_slots_stride=6), dict(src_slots=FAKE, src_slots_stride=10),
+                dict(src_row_stride=63), dict(dst_row_stride=63), dict(src=None), dict(dst=None),
+                dict(dst_slots=None), dict(accept_len=None), dict(accept_nodes=None), dict(src_rows=-1),
+                dict(dst_rows=-1), dict(src_group_stride=-1), dict(G=1 << 40, row_bytes=1 << 40)):
+        assert commit(**bad) == E, bad
+    for none in (dict(B=0), dict(G=0), dict(row_bytes=0)):
+        assert commit(src=None, **none) == OK
+
+
+def plan(**kw):
+    a = dict(seq_lens=FAKE, accept_len=None, release=None, draft_offsets=None, B=4, k=4, total_drafts=0,
+             block_size=16, block_tables=FAKE, table_stride=8, max_blocks=8, held_blocks=FAKE, free_ring=FAKE,
+             ring_capacity=100, ring_state=FAKE, seq_lens_out=FAKE, held_out=FAKE, ring_state_out=FAKE,
+             positions=FAKE, slots=FAKE, stream=0)
+    a.update(kw)
+    return sd.specdec_plan_slots(**a)
+
+
+def test_plan_refusals():
+    for bad in (dict(B=-1), dict(B=sd.MAX_B + 1), dict(k=-1), dict(k=sd.MAX_PLAN_ROWS), dict(block_size=0),
+                dict(block_size=sd.MAX_PLAN_ROWS + 1), dict(max_blocks=0), dict(table_stride=7),
+                dict(ring_capacity=0), dict(draft_offsets=FAKE, total_drafts=-1),
+                dict(draft_offsets=FAKE, total_drafts=17), dict(seq_lens=None), dict(block_tables=None),
+                dict(held_blocks=None), dict(free_ring=None), dict(ring_state=None), dict(seq_lens_out=None),
+                dict(held_out=None), dict(ring_state_out=None), dict(positions=None), dict(slots=None)):
+        assert plan(**bad) == E, bad
+    assert plan(B=0, seq_lens=None) == OK
+
+
+def test_host_tensors_are_refused():
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    ver = sd.Verifier(torch.device("cuda", 0))
+    with pytest.raises(ValueError):
+        ver.beam_select(torch.zeros(2, 3, 64), torch.zeros(2, 3), 3)
+    with pytest.raises(ValueError):
+        sd.reorder_states(torch.zeros(1, 2, 3, 4, 5), i(2, 3))
+    with pytest.raises(ValueError):
+        sd.commit_path(torch.zeros(1, 2, 3, 4), i(2), i(2, 2), torch.zeros(1, 9, 4), torch.zeros(2, 3).long())
+    with pytest.raises(ValueError):
+        sd.plan_slots(i(2), i(2, 4), i(2), i(10), i(2), 16, k=3)
+
+
+class OnGpu1:
+    """Stands for a tensor of another GPU."""
+    device = torch.device("cuda", 1)
+    is_cuda = True
+    dtype = torch.float32
+    shape = (1, 2, 3, 4, 5)
+
+    def dim(self):
+        return 5
+
+    def numel(self):
+        return 2
+
+
+def test_other_devices_are_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = OnGpu1()
+    with pytest.raises(ValueError, match="current device"):
+        sd.Verifier(torch.device("cuda", 0)).beam_select(x, x, 3)
+    with pytest.raises(ValueError, match="current device"):
+        sd.reorder_states(x, x)
+    with pytest.raises(ValueError, match="current device"):
+        sd.commit_path(x, x, x, x, x)
+    with pytest.raises(ValueError, match="current device"):
+        sd.plan_slots(x, x, x, x, x, 16)
+
+
+def test_outgrown_workspaces_are_kept(monkeypatch):
+    """A captured graph holds the workspace's address: growing the workspace
+    for a larger call must not free the smaller one."""
+    monkeypatch.setattr(sd, "specdec_workspace_init", lambda ws, n, stream=None: sd.SPECDEC_OK)
+    ver = sd.Verifier(torch.device("cpu"))
+    first, n = ver.workspace(1000)
+    ver.workspace(5000)
+    assert ver._ws is not first and any(w is first for w in ver._outgrown)
