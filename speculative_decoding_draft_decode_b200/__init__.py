@@ -21,7 +21,9 @@ There is no CPU fallback: if the CUDA library is missing, loading it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional
 
 __all__ = [
@@ -332,6 +334,7 @@ def ngram_propose(tokens, lengths, n_min: int = 2, n_max: int = 5, k: int = 4, p
     return (d[:, :k], n, off, packed) if pack else (d[:, :k], n)
 
 
+@functools.lru_cache(maxsize=1024)
 def specdec_workspace_size_beam(B: int, W: int, K: int, V: int, dtype: int) -> int:
     return lib().specdec_workspace_size_beam(B, W, K, V, dtype)
 
@@ -371,19 +374,41 @@ def specdec_plan_slots(seq_lens, accept_len, release, draft_offsets, B, k, total
 
 
 # ---------------------------------------------------------------------------
-# The caches around a verify step (torch layer)
+# The caches around a verify step (torch layer).  These calls enqueue kernels
+# of a few microseconds, so their checks are kept to a few attribute reads.
 # ---------------------------------------------------------------------------
-def _typed(t, dtype, shape, name):
-    """t, checked to be a contiguous tensor of that type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+def _current(t):
+    """The current device, for a call whose arrays are on a GPU."""
+    if not t.is_cuda:
+        _on_current_device(t)
+    import torch
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, cur):
+    """The stream handle of a call on the current device `cur`."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(cur)
+    return _stream(stream)
+
+
+def _want(t, dtype, shape, cur, name):
+    """Address of t, checked to be a contiguous tensor of that type and shape
+    on the current device `cur`."""
+    if t.get_device() != cur:
+        _on_current_device(t)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, list(shape)))
-    return t
+    return t.data_ptr()
 
 
 def _span(t):
     """First and last byte + 1 of the memory a tensor's elements lie in."""
-    n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
     at = t.data_ptr()
+    if t.is_contiguous():
+        return at, at + t.numel() * t.element_size()
+    n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
     return at, at + n * t.element_size()
 
 
@@ -392,13 +417,13 @@ def _overlap(a, b):
     return a0 < b1 and b0 < a1
 
 
-def _row_elems(t, dims, name):
-    """Elements of a row: the dimensions from `dims` on, which must lie one behind the other."""
+def _row_elems(shape, strides, lead, name):
+    """Elements of a row: the dimensions from `lead` on, which must lie one behind the other."""
     n = 1
-    for d in range(t.dim() - 1, dims - 1, -1):
-        if t.shape[d] != 1 and t.stride(d) != n:
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if strides[d] != n and shape[d] != 1:
             raise ValueError("%s: the dimensions of a row must be contiguous" % name)
-        n *= t.shape[d]
+        n *= shape[d]
     return n
 
 
@@ -410,6 +435,9 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
+_five = struct.Struct("5q").pack
+
+
 def reorder_states(states, parents, lengths=None, time_dim: int = 3, stream=None, out=None):
     """Row (b, i) of every group becomes row (b, parents[b, i]) over the
     positions below lengths[b] (all of them without lengths), after a beam
@@ -419,38 +447,61 @@ def reorder_states(states, parents, lengths=None, time_dim: int = 3, stream=None
     outside [0, W) is left as it is.  In place, or into `out` (same shape and
     type, no overlap).  Returns what was written."""
     import torch
-    to = states if out is None else out
-    if time_dim not in (3, 4) or states.dim() <= time_dim:
-        raise ValueError("states must be [G, B, W, T, ...] (time_dim 3) or [G, B, W, H, T, ...] (time_dim 4)")
-    if to.shape != states.shape or to.dtype != states.dtype:
-        raise ValueError("out must have the shape and type of states")
-    _on_current_device(states, to, parents, lengths, stream=stream)
     shape = states.shape
-    G, B, W, T = shape[0], shape[1], shape[2], shape[time_dim]
-    H = shape[3] if time_dim == 4 else 1
-    _typed(parents, torch.int32, (B, W), "parents")
-    if lengths is not None:
-        _typed(lengths, torch.int32, (B,), "lengths")
+    if (time_dim != 3 and time_dim != 4) or len(shape) <= time_dim:
+        raise ValueError("states must be [G, B, W, T, ...] (time_dim 3) or [G, B, W, H, T, ...] (time_dim 4)")
+    cur = _current(states)
+    if states.get_device() != cur or stream is not None:
+        _on_current_device(states, stream=stream)
+    G, B, W = shape[:3]
+    p = _want(parents, torch.int32, (B, W), cur, "parents")
+    n = None if lengths is None else _want(lengths, torch.int32, (B,), cur, "lengths")
     es = states.element_size()
-    row = _row_elems(states, time_dim + 1, "states") * es
+    strides = states.stride()
+    row = _row_elems(shape, strides, time_dim + 1, "states") * es
+    at = src = states.data_ptr()
+    to, dst = states, strides
+    if out is not None and out is not states:
+        to, dst, at = out, out.stride(), out.data_ptr()
+        if out.get_device() != cur:
+            _on_current_device(out)
+        if out.shape != shape or out.dtype is not states.dtype:
+            raise ValueError("out must have the shape and type of states")
+        _row_elems(shape, dst, time_dim + 1, "out")
     if to.numel() == 0:
         return to
-    strides = [s * es for s in states.stride()[:time_dim + 1]]
-    if to is states or (to.data_ptr() == states.data_ptr() and to.stride() == states.stride()):
-        dst_strides = strides
-    else:
-        _row_elems(to, time_dim + 1, "out")
-        dst_strides = [s * es for s in to.stride()[:time_dim + 1]]
-        if _overlap(states, to):
-            raise ValueError("out overlaps states: pass none to reorder in place")
-    if any(s < row and n > 1 for s, n in zip(dst_strides, shape)):
-        raise ValueError("the rows written must not share memory")
+    if to is not states and not (at == src and dst == strides) and _overlap(states, to):
+        raise ValueError("out overlaps states: pass none to reorder in place")
     if time_dim == 3:
-        strides = [*strides[:3], 0, strides[3]]
-        dst_strides = [*dst_strides[:3], 0, dst_strides[3]]
-    _check(specdec_reorder_states(states, to, parents, lengths, G, B, W, H, T, row, strides, dst_strides, stream),
+        g, b, w, t = dst[:4]
+        h, H, T, sh = 0, 1, shape[3], 0
+        sg, sb, sw, st = strides[:4]
+    else:
+        g, b, w, h, t = dst[:5]
+        H, T = shape[3:5]
+        sg, sb, sw, sh, st = strides[:5]
+    least = row // es
+    if (g < least and G > 1) or (b < least and B > 1) or (w < least and W > 1) or (h < least and H > 1) \
+            or (t < least and T > 1):
+        raise ValueError("the rows written must not share memory")
+    _check(lib().specdec_reorder_states(src, at, p, n, G, B, W, H, T, row,
+                                        _five(sg * es, sb * es, sw * es, sh * es, st * es),
+                                        _five(g * es, b * es, w * es, h * es, t * es), _raw_stream(stream, cur)),
            "reorder_states")
     return to
+
+
+def _slot_table(t, B, cur, name):
+    """Address, columns and row stride of an int64 [B, n] table of slots."""
+    import torch
+    if t.get_device() != cur:
+        _on_current_device(t)
+    if t.dtype is torch.int64 and t.dim() == 2:
+        rows, n = t.shape
+        rs, es = t.stride()
+        if rows == B and (es == 1 or n == 1) and (rs >= n or B == 1):
+            return t.data_ptr(), n, rs if rs > n else n
+    raise ValueError("%s must be an int64 [B, n] tensor with contiguous rows" % name)
 
 
 def commit_path(src, accept_len, accept_nodes, dst, dst_slots, src_slots=None, stream=None):
@@ -462,48 +513,54 @@ def commit_path(src, accept_len, accept_nodes, dst, dst_slots, src_slots=None, s
     slots of plan_slots with k = N: slots.view(B, N + 1)).  src and dst may be
     one cache when src_slots and dst_slots hold the same slots.  Returns dst."""
     import torch
-    _on_current_device(src, accept_len, accept_nodes, dst, dst_slots, src_slots, stream=stream)
+    cur = _current(src)
+    if src.get_device() != cur or dst.get_device() != cur or stream is not None:
+        _on_current_device(src, dst, stream=stream)
     if accept_nodes.dim() != 2:
         raise ValueError("accept_nodes must be [B, max_depth]")
-    B, depth = accept_nodes.shape
-    _typed(accept_nodes, torch.int32, (B, depth), "accept_nodes")
-    _typed(accept_len, torch.int32, (B,), "accept_len")
+    B, depth = shape = accept_nodes.shape
+    nodes_at = _want(accept_nodes, torch.int32, shape, cur, "accept_nodes")
+    len_at = _want(accept_len, torch.int32, (B,), cur, "accept_len")
     lead = 3 if src_slots is None else 2
-    if src.dim() < lead or dst.dim() < 2 or src.dtype != dst.dtype or src.shape[lead:] != dst.shape[2:] \
-            or src.shape[0] != dst.shape[0]:
+    ss, ds = src.shape, dst.shape
+    if len(ss) < lead or len(ds) < 2 or src.dtype is not dst.dtype or ss[lead:] != ds[2:] or ss[0] != ds[0]:
         raise ValueError("src must be [G, B, N + 1, ...] (with src_slots [G, S, ...]) and dst [G, slots, ...] of its type")
-    for name, t in (("dst_slots", dst_slots), ("src_slots", src_slots)):
-        if t is not None and (t.dtype != torch.int64 or t.dim() != 2 or t.shape[0] != B or t.stride(1) != 1
-                              or (B > 1 and t.stride(0) < t.shape[1])):
-            raise ValueError("%s must be an int64 [B, n] tensor with contiguous rows" % name)
-    if dst_slots.shape[1] < depth + 1:
+    to_at, n, to_stride = _slot_table(dst_slots, B, cur, "dst_slots")
+    if n < depth + 1:
         raise ValueError("dst_slots must have max_depth + 1 columns at least")
     es = src.element_size()
-    row = _row_elems(src, lead, "src") * es
-    _row_elems(dst, 2, "dst")
+    s_src, s_dst = src.stride(), dst.stride()
+    row = _row_elems(ss, s_src, lead, "src")
+    _row_elems(ds, s_dst, 2, "dst")
+    src_at, dst_at = src.data_ptr(), dst.data_ptr()
+    if src_slots is None:
+        if ss[1] != B:
+            raise ValueError("src must be [G, B, N + 1, ...]")
+        from_at, src_rows, from_stride = None, 0, 0
+        nodes = ss[2]
+        sg, sb, sr = s_src[:3]
+        if nodes == 1 and sr < row:
+            sr = row
+        same = False
+    else:
+        from_at, nodes, from_stride = _slot_table(src_slots, B, cur, "src_slots")
+        src_rows, sb = ss[1], 0
+        sg, sr = s_src[:2]
+        if src_rows == 1 and sr < row:
+            sr = row
+        same = src_at == dst_at and s_src == s_dst
     if src.numel() == 0 or dst.numel() == 0 or B == 0:
         return dst
-    if src_slots is None:
-        if src.shape[1] != B:
-            raise ValueError("src must be [G, B, N + 1, ...]")
-        nodes, src_rows, ss = src.shape[2], 0, 0
-        sg, sb, sr = (s * es for s in src.stride()[:3])
-        sr = max(sr, row) if nodes == 1 else sr
-    else:
-        nodes, src_rows, ss = src_slots.shape[1], src.shape[1], max(src_slots.stride(0), src_slots.shape[1])
-        sg, sr = (s * es for s in src.stride()[:2])
-        sr = max(sr, row) if src_rows == 1 else sr
-        sb = 0
-    dg, dr = (s * es for s in dst.stride()[:2])
-    dr = max(dr, row) if dst.shape[1] == 1 else dr
-    same = src_slots is not None and src.data_ptr() == dst.data_ptr() and src.stride() == dst.stride()
+    dg, dr = s_dst[:2]
+    if ds[1] == 1 and dr < row:
+        dr = row
     if not same and _overlap(src, dst):
         raise ValueError("src and dst overlap: in place both must be the same cache, with src_slots")
-    if dst.shape[0] > 1 and dg < row:
+    if dg < row and ds[0] > 1:
         raise ValueError("the rows written must not share memory")
-    _check(specdec_commit_path(src, sg, sb, sr, src_slots, ss, src_rows, dst, dg, dr, dst_slots,
-                               max(dst_slots.stride(0), dst_slots.shape[1]), dst.shape[1], accept_len, accept_nodes,
-                               src.shape[0], B, nodes - 1, depth, row, stream), "commit_path")
+    _check(lib().specdec_commit_path(src_at, sg * es, sb * es, sr * es, from_at, from_stride, src_rows, dst_at, dg * es,
+                                     dr * es, to_at, to_stride, ds[1], len_at, nodes_at, ss[0], B, nodes - 1, depth,
+                                     row * es, _raw_stream(stream, cur)), "commit_path")
     return dst
 
 
@@ -517,44 +574,45 @@ def plan_slots(seq_lens, block_tables, held_blocks, free_ring, ring_state, block
     ring_state, positions int64 [rows], slots int64 [rows]): the new values,
     in `out` when given (whose first three may be the arrays they replace)."""
     import torch
+    i32, i64 = torch.int32, torch.int64
+    cur = _current(seq_lens)
+    if stream is not None:
+        _on_current_device(stream=stream)
     B = seq_lens.numel()
-    _on_current_device(seq_lens, block_tables, held_blocks, free_ring, ring_state, draft_offsets, accept_len, release,
-                       *(out or ()), stream=stream)
-    i32 = torch.int32
-    _typed(seq_lens, i32, (B,), "seq_lens")
-    _typed(held_blocks, i32, (B,), "held_blocks")
-    if accept_len is not None:
-        _typed(accept_len, i32, (B,), "accept_len")
-    if release is not None:
-        _typed(release, i32, (B,), "release")
-    _typed(free_ring, i32, (free_ring.numel(),), "free_ring")
-    _typed(ring_state, i32, (2,), "ring_state")
-    if block_tables.dtype != i32 or block_tables.dim() != 2 or block_tables.shape[0] != B \
-            or block_tables.stride(1) != 1 or (B > 1 and block_tables.stride(0) < block_tables.shape[1]):
-        raise ValueError("block_tables must be an int32 [B, max_blocks] tensor with contiguous rows")
+    one = (B,)
     if draft_offsets is not None:
-        _typed(draft_offsets, i32, (B + 1,), "draft_offsets")
+        offsets_at = _want(draft_offsets, i32, (B + 1,), cur, "draft_offsets")
         rows = B + total_drafts
     else:
-        rows = B * (k + 1)
+        offsets_at, rows = None, B * (k + 1)
     if rows < 0:
         raise ValueError("k and total_drafts must not be negative")
+    ring = free_ring.numel()
+    if block_tables.get_device() != cur:
+        _on_current_device(block_tables)
+    if block_tables.dtype is not i32 or block_tables.dim() != 2:
+        raise ValueError("block_tables must be an int32 [B, max_blocks] tensor with contiguous rows")
+    nb, cols = block_tables.shape
+    ts, es = block_tables.stride()
+    if nb != B or (es != 1 and cols != 1) or (ts < cols and B > 1):
+        raise ValueError("block_tables must be an int32 [B, max_blocks] tensor with contiguous rows")
     if out is None:
         dev = seq_lens.device
         out = (torch.empty(B, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
                ring_state.clone() if B == 0 else torch.empty(2, dtype=i32, device=dev),
-               torch.empty(rows, dtype=torch.int64, device=dev), torch.empty(rows, dtype=torch.int64, device=dev))
+               torch.empty(rows, dtype=i64, device=dev), torch.empty(rows, dtype=i64, device=dev))
         _used_on(stream, *out)
-    else:
-        for t, dt, n, name in zip(out, (i32, i32, i32, torch.int64, torch.int64), (B, B, 2, rows, rows),
-                                  ("seq_lens", "held_blocks", "ring_state", "positions", "slots")):
-            _typed(t, dt, (n,), "out: " + name)
-    cols = block_tables.shape[1]
     lens, held, state, positions, slots = out
-    _check(specdec_plan_slots(seq_lens, accept_len, release, draft_offsets, B, k, total_drafts, block_size,
-                              block_tables, block_tables.stride(0) if B > 1 else cols, cols, held_blocks, free_ring,
-                              free_ring.numel(), ring_state, lens, held, state, positions, slots, stream),
-           "plan_slots")
+    _check(lib().specdec_plan_slots(
+        _want(seq_lens, i32, one, cur, "seq_lens"),
+        None if accept_len is None else _want(accept_len, i32, one, cur, "accept_len"),
+        None if release is None else _want(release, i32, one, cur, "release"),
+        offsets_at, B, k, total_drafts, block_size, block_tables.data_ptr(), ts if ts > cols else cols, cols,
+        _want(held_blocks, i32, one, cur, "held_blocks"), _want(free_ring, i32, (ring,), cur, "free_ring"), ring,
+        _want(ring_state, i32, (2,), cur, "ring_state"), _want(lens, i32, one, cur, "out: seq_lens"),
+        _want(held, i32, one, cur, "out: held_blocks"), _want(state, i32, (2,), cur, "out: ring_state"),
+        _want(positions, i64, (rows,), cur, "out: positions"), _want(slots, i64, (rows,), cur, "out: slots"),
+        _raw_stream(stream, cur)), "plan_slots")
     return lens, held, state, positions, slots
 
 
@@ -688,28 +746,31 @@ class Verifier:
         (scores float32 [B, num_beams], parents, tokens int32 [B, num_beams]),
         the best continuations in descending order."""
         import torch
-        _on_current_device(logits, beam_scores, finished, *(out or ()), stream=stream)
-        self._on_device(logits)
+        cur = _current(logits)
+        f32, i32 = torch.float32, torch.int32
+        if logits.get_device() != cur or stream is not None:
+            _on_current_device(logits, stream=stream)
+        if self.device.index != cur:
+            self._on_device(logits)
         dt = _dtype_code(logits)
         stride = _row_stride(logits, "logits")
         B, W, V = logits.shape
         K = num_beams
-        _typed(beam_scores, torch.float32, (B, W), "beam_scores")
-        if finished is not None:
-            _typed(finished, torch.int32, (B, W), "finished")
+        shape = (B, K if K > 0 else 0)
         if out is None:
             dev = logits.device
-            out = (torch.empty(B, max(K, 0), dtype=torch.float32, device=dev),
-                   torch.empty(B, max(K, 0), dtype=torch.int32, device=dev),
-                   torch.empty(B, max(K, 0), dtype=torch.int32, device=dev))
+            out = (torch.empty(shape, dtype=f32, device=dev), torch.empty(shape, dtype=i32, device=dev),
+                   torch.empty(shape, dtype=i32, device=dev))
             _used_on(stream, *out)
-        else:
-            for t, d, name in zip(out, (torch.float32, torch.int32, torch.int32), ("scores", "parents", "tokens")):
-                _typed(t, d, (B, K), "out: " + name)
         scores, parents, tokens = out
+        L = lib()
         ws, wsb = self.workspace(specdec_workspace_size_beam(B, W, K, V, dt), stream)
-        _check(specdec_beam_select(logits, dt, stride, beam_scores, finished, eos_token, B, W, K, V, scores, parents,
-                                   tokens, ws, wsb, stream), "beam_select")
+        _check(L.specdec_beam_select(
+            logits.data_ptr(), dt, stride, _want(beam_scores, f32, (B, W), cur, "beam_scores"),
+            None if finished is None else _want(finished, i32, (B, W), cur, "finished"), eos_token, B, W, K, V,
+            _want(scores, f32, shape, cur, "out: scores"), _want(parents, i32, shape, cur, "out: parents"),
+            _want(tokens, i32, shape, cur, "out: tokens"), None if ws is None else ws.data_ptr(), wsb,
+            _raw_stream(stream, cur)), "beam_select")
         return scores, parents, tokens
 
     def tree(self, logits, parents, node_tokens, max_depth: int, stream=None, out=None):

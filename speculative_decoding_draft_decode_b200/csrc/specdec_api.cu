@@ -12,6 +12,7 @@
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
+#include <stdlib.h>
 
 #include <atomic>
 
@@ -217,6 +218,17 @@ namespace {
 
 // Beam selection: the chunks' statistics and best keys, behind the fixed area
 // (which it does not touch).
+#ifndef BEAM_CHUNK
+#define BEAM_CHUNK 4096
+#endif
+int beam_chunk_vecs(int64_t rows, int nv) {
+    static const char* e = getenv("BEAM_CHUNK");
+    if (e) return atoi(e);
+    (void)rows;
+    (void)nv;
+    return BEAM_CHUNK;
+}
+
 struct BeamLayout {
     int cpr = 0;
     size_t stats = 0, keys = 0, total = 0;
@@ -225,7 +237,9 @@ struct BeamLayout {
 BeamLayout make_beam_layout(int B, int W, int K, int V, specdec_dtype dtype) {
     BeamLayout L;
     const int ve = vec_elems(dtype);
-    L.cpr = static_cast<int>(chunks_per_row(V / ve, ve));
+    const int nv = V / ve;
+    const int chunk = beam_chunk_vecs(static_cast<int64_t>(B) * W, nv);
+    L.cpr = nv > chunk ? (nv + chunk - 1) / chunk : 1;
     const size_t chunks = static_cast<size_t>(B) * static_cast<size_t>(W) * static_cast<size_t>(L.cpr);
     L.stats = kPartialBase;
     L.keys = align_up(L.stats + chunks * sizeof(BeamStat), 256);
@@ -239,7 +253,8 @@ specdec_status launch_beam(const BeamParams& P, cudaStream_t stream) {
     if (P.cpr > 65535) return SPECDEC_ERR_UNSUPPORTED;  // grid limit
     const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(P.cpr));
     if (launch_pdl(beam_pass_kernel<Tag, Tag::VEC>, grid, 0, stream, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
-    if (launch_pdl(beam_merge_kernel, dim3(static_cast<unsigned>(P.B)), 0, stream, P) != cudaSuccess)
+    const int warps = P.W <= 8 ? 8 : P.W <= 16 ? 16 : 32;  // a warp per beam
+    if (launch_pdl(beam_merge_kernel, dim3(static_cast<unsigned>(P.B)), 0, stream, P, 32 * warps) != cudaSuccess)
         return SPECDEC_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }

@@ -126,6 +126,9 @@ class OnGpu1:
     def dim(self):
         return 5
 
+    def get_device(self):
+        return 1
+
     def numel(self):
         return 2
 
