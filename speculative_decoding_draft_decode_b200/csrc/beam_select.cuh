@@ -5,18 +5,17 @@
 // probability of the branches) and "Medusa" (candidates form a tree): the
 // level's candidates are every (beam w, token v) with
 //   c = s_w + l_wv - log sum_v' exp(l_wv'),
-// and the K largest are kept, equal values in order of w V + v.  A row adds
-// the same number to all its logits, so a row's K best are its K largest
-// logits (lowest index first among equals), whatever its sum turns out to be:
-// the logits are read once.
+// and the K largest are kept, equal values in order of w V + v.
 //
-// beam_pass_kernel: one CTA per (row, chunk of up to kU 16-byte vectors per
-// thread).  The chunk stays in registers: its maximum, a threshold that at
-// least K of its elements reach, sum exp(l - max), and its K best keys.
-// beam_merge_kernel: one CTA per request: the rows' sums, a bound that K
-// candidates reach, and the order of the candidates above it in fp64.
-// Nothing is shared between CTAs but the partials, and every sum has a fixed
-// order: the results do not vary from run to run.
+// beam_stream reads the logits once.  A warp takes a segment of a row,
+// tile by tile (128 vectors of 16 bytes, 4 a lane, loaded one tile ahead), and
+// keeps sum exp(l - ref) and every tile's largest logit.  Nothing is selected
+// here, so warps need neither thresholds nor one another.
+// beam_merge, one CTA per request: the rows' sums, then the K best
+// tiles by (c of the largest logit, position).  An element of any other tile
+// has K elements before it (the largest ones of these K tiles: greater, or
+// equal and earlier), so only K tiles are read again.  Values are ordered in
+// fp64.  Every sum has a fixed order: results do not vary from run to run.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -31,11 +30,12 @@
 namespace specdec {
 
 constexpr int kMaxBeams = 32;    // beams per request, and beams selected
-constexpr int kBeamMerge = 1024;  // candidates of a request held in shared memory
+constexpr int kTileU = 4;        // 16-byte vectors of a tile per lane
+constexpr int kTileVecs = 32 * kTileU;
 
 struct BeamStat {
-    double M;  // a value near the chunk's largest logit
-    double S;  // sum exp(l - M) over the chunk; NaN for a NaN or +inf logit
+    double M;  // a value near the segment's largest logit
+    double S;  // sum exp(l - M) over the segment; NaN for a NaN or +inf logit
 };
 
 struct BeamParams {
@@ -45,10 +45,12 @@ struct BeamParams {
     const int32_t* finished;  // [B, W] or null
     int B, W, K, V;
     int eos;
-    int cpr;             // chunks per row
-    BeamStat* stats;     // [B W, cpr]
-    uint64_t* keys;      // [B W, cpr, K] the chunks' best, descending, 0 past the end
-    float* out_scores;   // [B, K]
+    int tiles;        // tiles per row
+    int seg_tiles;    // tiles of a segment
+    int segs;         // segments per row
+    BeamStat* stats;  // [B W, segs]
+    float* peaks;     // [B W, tiles] largest logit of each tile (-inf: none above it)
+    float* out_scores;  // [B, K]
     int32_t* out_parents;
     int32_t* out_tokens;
 };
@@ -57,13 +59,14 @@ struct BeamParams {
 // finished.
 __device__ __forceinline__ bool beam_streams(const BeamParams& P, int64_t r) {
     const float s = __ldg(&P.scores[r]);
-    if (!(s > -INFINITY && s < INFINITY)) return false;
-    return P.finished == nullptr || __ldg(&P.finished[r]) == 0;
+    const int f = P.finished != nullptr ? __ldg(&P.finished[r]) : 0;
+    return s > -INFINITY && s < INFINITY && f == 0;
 }
 
 // The vectors of a row: elements before the first 16-byte boundary (the
 // head), nv full vectors, and the elements behind them (the tail).  Rows need
-// no alignment beyond their element's.
+// no alignment beyond their element's.  The head belongs to the first tile and
+// the tail to the last one.
 struct RowCut {
     int head, nv, tail;
 };
@@ -84,42 +87,18 @@ __device__ __forceinline__ uint4 minus_inf_vec() {
     return make_uint4(x, x, x, x);
 }
 
-// A value that at least K of the CTA's threads reach, from one ordered value
-// per thread (INT_MIN: none): the K-th largest of the 32 values that the
-// warps' 32 / warps largest lanes make up.  pool holds 32 words; one CTA
-// barrier.  x: the bound (INT_MIN if fewer than K values are there), y: the
-// largest value.
-__device__ __forceinline__ int2 cta_kth(int v, int K, int warps, int* pool) {
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int m = 32 / warps;
-    int mine = INT_MIN;
-    for (int i = 0; i < m; ++i) {
-        const int x = __reduce_max_sync(FULL_MASK, v);
-        if (lane == i) mine = x;
-        const unsigned who = __ballot_sync(FULL_MASK, v == x);
-        if (lane == __ffs(who) - 1) v = INT_MIN;
+// The K-th largest of the warp's 32 ordered values (INT_MIN: none).  Each lane
+// counts the values before its own.
+__device__ __forceinline__ int warp_kth(int p, int K) {
+    const int lane = threadIdx.x & 31;
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const int x = __shfl_sync(FULL_MASK, p, i);
+        rank += x > p || (x == p && i < lane) ? 1 : 0;
     }
-    if (lane < m) pool[wp * m + lane] = mine;
-    __syncthreads();
-    int p = pool[lane];
-    int2 r;
-    r.y = __reduce_max_sync(FULL_MASK, p);
-    if (K <= 16) {  // take the K - 1 largest out
-        r.x = r.y;
-        for (int i = 1; i < K; ++i) {
-            const unsigned who = __ballot_sync(FULL_MASK, p == r.x);
-            if (lane == __ffs(who) - 1) p = INT_MIN;
-            r.x = __reduce_max_sync(FULL_MASK, p);
-        }
-    } else {  // take the 32 - K least out
-        r.x = __reduce_min_sync(FULL_MASK, p);
-        for (int i = K; i < 32; ++i) {
-            const unsigned who = __ballot_sync(FULL_MASK, p == r.x);
-            if (lane == __ffs(who) - 1) p = INT_MAX;
-            r.x = __reduce_min_sync(FULL_MASK, p);
-        }
-    }
-    return r;
+    const unsigned who = __ballot_sync(FULL_MASK, rank == K - 1);
+    return __shfl_sync(FULL_MASK, p, __ffs(who) - 1);
 }
 
 __device__ __forceinline__ uint32_t max_bf162(uint32_t a, uint32_t b) {
@@ -151,34 +130,54 @@ __device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c
     return r;
 }
 
-#ifndef BEAM_MINB
-#define BEAM_MINB 5
-#endif
-constexpr int kBeamBatch = 4;    // vectors a thread loads at a time, one batch ahead
-constexpr int kBeamVecs = 1024;   // vectors of a chunk that may hold candidates
-constexpr int kBeamCand = 512;   // candidates of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 
-struct BeamSmem {
-    uint4 vec[kBeamVecs];
-    int at[kBeamVecs];  // their vector numbers
-    uint64_t cand[kBeamCand];
-    uint64_t red[NWARPS];
-    double S[NWARPS];
-    float ref[NWARPS];
-    int pool[32];
-    int vecs, cands;
+// A tile as a lane holds it: vectors [j, j + 128) of the row, and in the first
+// and last tile one element of the head or tail (xe, number ie; -inf: none).
+template <class Tag, int VEC>
+struct BeamTile {
+    using Elem = typename Tag::storage;
+    uint4 w[kTileU];
+    __device__ __forceinline__ void load(const Elem* row, const RowCut& cut, int tile) {
+        const int lane = threadIdx.x & 31, j = tile * kTileVecs;
+        const Elem* p = row + cut.head + static_cast<int64_t>(j + lane) * VEC;
+        if (j + kTileVecs <= cut.nv) {
+#pragma unroll
+            for (int u = 0; u < kTileU; ++u) w[u] = ld_stream_v4(p + u * 32 * VEC);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kTileU; ++u) {
+                w[u] = minus_inf_vec<Tag>();
+                if (j + u * 32 + lane < cut.nv) w[u] = ld_stream_v4(p + u * 32 * VEC);
+            }
+        }
+    }
+    // The largest element (NaN ignored).
+    __device__ __forceinline__ float most() const {
+        if constexpr (sizeof(Elem) == 2) {
+            const uint4 m = make_uint4(max_bf162(max_bf162(w[0].x, w[1].x), max_bf162(w[2].x, w[3].x)),
+                                       max_bf162(max_bf162(w[0].y, w[1].y), max_bf162(w[2].y, w[3].y)),
+                                       max_bf162(max_bf162(w[0].z, w[1].z), max_bf162(w[2].z, w[3].z)),
+                                       max_bf162(max_bf162(w[0].w, w[1].w), max_bf162(w[2].w, w[3].w)));
+            return VecOps<Tag, VEC>::vmax(m);
+        } else {
+            return fmaxf(fmaxf(VecOps<Tag, VEC>::vmax(w[0]), VecOps<Tag, VEC>::vmax(w[1])),
+                         fmaxf(VecOps<Tag, VEC>::vmax(w[2]), VecOps<Tag, VEC>::vmax(w[3])));
+        }
+    }
 };
 
-// What a thread carries through its part of a chunk.
-struct BeamThread {
-    float th;    // K elements of the chunk reach it
-    float hit;   // elements below it are no candidates of the batches to come
-    float ref;   // S counts exp(l - beam_ref(ref))
-    bool known;  // CTA-uniform: K elements above -inf have been seen
-    bool flood;  // many vectors reach the threshold
-    double S;
-};
+// This lane's element of the head (first tile) or tail (last tile): its value,
+// -inf if it has none, and its number.  Head and tail have at most 7 elements.
+template <class Tag>
+__device__ __forceinline__ float beam_end(const typename Tag::storage* row, const RowCut& cut, int V, bool first,
+                                          bool last, int& ie) {
+    const int lane = threadIdx.x & 31;
+    ie = -1;
+    if (first && lane < cut.head) ie = lane;
+    if (last && lane >= 8 && lane < 8 + cut.tail) ie = V - cut.tail + lane - 8;
+    return ie >= 0 ? load_scalar<Tag>(row + ie) : -INFINITY;
+}
 
 // Each term is taken as 2^(l c - E) with one rounding in the exponent: c is
 // log2 e in fp32 and E = ref c in fp32, so the terms count from E / c exactly,
@@ -193,13 +192,13 @@ __device__ __forceinline__ float beam_term(float x, float ref) {
     return ex2_sfu(beam_far(ref) ? (x - ref) * kLog2e : __fmaf_rn(x, kLog2e, -__fmul_rn(ref, kLog2e)));
 }
 
-// The sum of a batch's terms, fp32: 2 x 16 (bf16) or 2 x 8 (fp32) of them.
+// The sum of a tile's terms, fp32: 2 x 16 (bf16) or 2 x 8 (fp32) of them.
 template <class Tag, int VEC>
-__device__ __forceinline__ float beam_batch_sum(const uint4 (&w)[kBeamBatch], float ref) {
+__device__ __forceinline__ float beam_sum(const uint4 (&w)[kTileU], float ref) {
     if (beam_far(ref)) {
         float s = 0.0f;
 #pragma unroll 1
-        for (int i = 0; i < kBeamBatch * VEC; ++i) {
+        for (int i = 0; i < kTileU * VEC; ++i) {
             const int u = i / VEC;
             const uint4 x = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
             s += beam_term(VecOps<Tag, VEC>::elem(x, i % VEC), ref);
@@ -210,7 +209,7 @@ __device__ __forceinline__ float beam_batch_sum(const uint4 (&w)[kBeamBatch], fl
     const uint64_t minus = f32x2(-E, -E), scale = f32x2(kLog2e, kLog2e);
     uint64_t s = f32x2(0.0f, 0.0f);
 #pragma unroll
-    for (int u = 0; u < kBeamBatch; ++u)
+    for (int u = 0; u < kTileU; ++u)
 #pragma unroll
         for (int q = 0; q < VEC; q += 2) {
             const uint64_t x = f32x2(VecOps<Tag, VEC>::elem(w[u], q), VecOps<Tag, VEC>::elem(w[u], q + 1));
@@ -221,272 +220,115 @@ __device__ __forceinline__ float beam_batch_sum(const uint4 (&w)[kBeamBatch], fl
     return r.x + r.y;
 }
 
-// The largest element of a batch (NaN ignored).
-template <class Tag, int VEC>
-__device__ __forceinline__ float beam_batch_max(const uint4 (&w)[kBeamBatch]) {
-    if constexpr (sizeof(typename Tag::storage) == 2) {
-        const uint4 m = make_uint4(max_bf162(max_bf162(w[0].x, w[1].x), max_bf162(w[2].x, w[3].x)),
-                                   max_bf162(max_bf162(w[0].y, w[1].y), max_bf162(w[2].y, w[3].y)),
-                                   max_bf162(max_bf162(w[0].z, w[1].z), max_bf162(w[2].z, w[3].z)),
-                                   max_bf162(max_bf162(w[0].w, w[1].w), max_bf162(w[2].w, w[3].w)));
-        return VecOps<Tag, VEC>::vmax(m);
-    } else {
-        return fmaxf(fmaxf(VecOps<Tag, VEC>::vmax(w[0]), VecOps<Tag, VEC>::vmax(w[1])),
-                     fmaxf(VecOps<Tag, VEC>::vmax(w[2]), VecOps<Tag, VEC>::vmax(w[3])));
-    }
-}
-
-// A value above the reference by more than kBeamRaise: the sum goes over to it
-// (terms stay below 2^6 and the fp32 sums far from overflow).
+// A tile's largest logit above the reference by more than this: the sum goes
+// over to it (terms stay below 2^6, far from overflow).
 constexpr float kBeamRaise = 4.0f;
-__device__ __forceinline__ void beam_raise(BeamThread& st, float m) {
-    if (m > st.ref + kBeamRaise) {
-        st.S *= exp(beam_ref(st.ref) - beam_ref(m));
-        st.ref = m;
-    }
+
+// A sum over to another reference.
+__device__ __noinline__ double beam_carry(double S, float from, float to) {
+    return S == 0.0 ? 0.0 : S * exp(beam_ref(from) - beam_ref(to));
 }
 
-// The least float above x (both zeros count as +0).
-__device__ __forceinline__ float next_up(float x) { return x == 0.0f ? __int_as_float(1) : from_ord_i32(ord_i32(x) + 1); }
-
+// A warp's segment: tiles [t0, t1) of row r.
 template <class Tag, int VEC>
-__device__ __forceinline__ void beam_batch(BeamThread& st, const uint4 (&w)[kBeamBatch], int j, int K, BeamSmem& sm) {
-    const int lane = threadIdx.x & 31;
-    const float tm = beam_batch_max<Tag, VEC>(w);
-    const bool first = !st.known;
-    bool raised = false;
-    if (first) {
-        __syncthreads();
-        const int2 k = cta_kth(ord_i32(tm), K, NWARPS, sm.pool);
-        if (k.x >= ord_i32(-FLT_MAX)) {
-            st.known = true;
-            st.th = st.hit = from_ord_i32(k.x);
-            raised = true;
-        }
-        const float top = from_ord_i32(k.y);  // one reference for the CTA
-        if (top > -INFINITY) beam_raise(st, top);
-    } else if (__any_sync(FULL_MASK, st.flood)) {
-        // Many vectors reach the threshold: raise it to the K-th largest lane
-        // maximum of this warp's batch.
-        int v = ord_i32(tm), x = INT_MIN;
-        for (int i = 0; i < K; ++i) {
-            x = __reduce_max_sync(FULL_MASK, v);
-            const unsigned who = __ballot_sync(FULL_MASK, v == x);
-            if (lane == __ffs(who) - 1) v = INT_MIN;
-        }
-        if (x >= ord_i32(-FLT_MAX) && from_ord_i32(x) > st.th) {
-            st.th = st.hit = from_ord_i32(x);
-            raised = true;
-        }
-    }
-    if (tm >= st.hit) {
-        beam_raise(st, tm);  // the reference is never below the threshold - kBeamRaise
-#pragma unroll
-        for (int u = 0; u < kBeamBatch; ++u)
-            if (VecOps<Tag, VEC>::vmax(w[u]) >= st.hit) {
-                const int at = atomicAdd(&sm.vecs, 1);
-                if (at < kBeamVecs) {
-                    sm.vec[at] = w[u];
-                    sm.at[at] = j + u * NT;
-                }
-                st.flood |= at > kBeamVecs / 4;
-            }
-    }
-    // The K elements that reach a threshold are in the batch that gave it:
-    // elements of later batches that only equal it come behind them.
-    if (raised) st.hit = next_up(st.th);
-    st.S += static_cast<double>(beam_batch_sum<Tag, VEC>(w, st.ref));
-}
-
-// The K best keys of a chunk whose candidates do not fit (runs of equal
-// values): the largest key below the last one found, K times, over the
-// vectors put aside or, if there were more than kBeamVecs, over the chunk read
-// again.  CTA-collective.
-template <class Tag, int VEC>
-__device__ __noinline__ void beam_chunk_ties(const typename Tag::storage* row, RowCut cut, int v0, int cnt, bool ends,
-                                             float th, int K, BeamSmem& sm, uint64_t* out) {
-    const int t = threadIdx.x;
-    const int vecs = sm.vecs;
-    const int first = cut.head + v0 * VEC, n = vecs <= kBeamVecs ? 0 : cnt * VEC;
-    const int extra = ends ? cut.head + cut.tail : 0;
-    uint64_t last = ~0ull;
-    for (int i = 0; i < K; ++i) {
-        uint64_t best = 0ull;
-        auto offer = [&](float f, int x) {
-            if (f >= th) {
-                const uint64_t k = make_key(f, x);
-                if (k < last && k > best) best = k;
-            }
-        };
-        if (vecs <= kBeamVecs)
-            for (int j = t; j < vecs; j += NT) {
-                const uint4 w = sm.vec[j];
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) offer(VecOps<Tag, VEC>::elem(w, q), first + sm.at[j] * VEC + q);
-            }
-        for (int j = t; j < n + extra; j += NT) {
-            int x = first + j;
-            if (j >= n) x = j - n < cut.head ? j - n : cut.head + cut.nv * VEC + (j - n - cut.head);
-            offer(load_scalar<Tag>(row + x), x);
-        }
-        best = block_max_u64(best, sm.red);
-        if (t == 0) out[i] = best;
-        last = best;
-    }
-}
-
-template <class Tag, int VEC>
-__global__ void __launch_bounds__(NT, BEAM_MINB) beam_pass_kernel(const BeamParams P) {
-    __shared__ BeamSmem sm;
+__device__ __forceinline__ void beam_stream(const BeamParams& P, int64_t r, int seg) {
     using Elem = typename Tag::storage;
-    const int t = threadIdx.x, lane = t & 31, wp = t >> 5;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t r = blockIdx.x;
-    const int sub = blockIdx.y;
-    if (!beam_streams(P, r)) return;  // CTA-uniform
+    const int lane = threadIdx.x & 31;
+    const int t0 = seg * P.seg_tiles, t1 = min(t0 + P.seg_tiles, P.tiles);
     const Elem* row = static_cast<const Elem*>(P.logits) + r * P.row_stride;
     const RowCut cut = cut_row<Tag, VEC>(row, P.V);
-    // the row's vectors are dealt evenly over its chunks
-    const int per = (cut.nv + P.cpr - 1) / P.cpr;
-    const int v0 = min(sub * per, cut.nv), cnt = min(per, cut.nv - v0);
-    const Elem* base = row + cut.head + static_cast<int64_t>(v0) * VEC;
-    auto load = [&](uint4 (&w)[kBeamBatch], int j) {
-        if (j - t + NT * kBeamBatch <= cnt) {  // CTA-uniform: a whole batch
-            const Elem* p = base + static_cast<int64_t>(j) * VEC;
-#pragma unroll
-            for (int u = 0; u < kBeamBatch; ++u) w[u] = ld_stream_v4(p + u * NT * VEC);
-            return;
-        }
-#pragma unroll
-        for (int u = 0; u < kBeamBatch; ++u) {
-            w[u] = minus_inf_vec<Tag>();
-            if (j + u * NT < cnt) w[u] = ld_stream_v4(base + static_cast<int64_t>(j + u * NT) * VEC);
-        }
+    float* peaks = P.peaks + r * P.tiles;
+    BeamTile<Tag, VEC> a;
+    a.load(row, cut, t0);
+    int ie;
+    const float xe = beam_end<Tag>(row, cut, P.V, t0 == 0, t1 == P.tiles, ie);
+    const bool is_head = ie >= 0 && ie < cut.head;
+    // The largest logit of a tile, for all lanes.
+    auto peak = [&](float m, int tile) {
+        if (tile == 0 && is_head) m = fmaxf(m, xe);
+        if (tile == P.tiles - 1 && ie >= 0 && !is_head) m = fmaxf(m, xe);
+        return from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(m)));
     };
-    uint4 wa[kBeamBatch], wb[kBeamBatch];
-    load(wa, t);
-    // the first chunk also takes the row's head and tail, one element a thread
-    float xe = -INFINITY;
-    int ie = 0;
-    if (sub == 0 && t < cut.head + cut.tail) {
-        ie = t < cut.head ? t : cut.head + cut.nv * VEC + (t - cut.head);
-        xe = load_scalar<Tag>(row + ie);
-    }
-    if (t == 0) sm.vecs = sm.cands = 0;
-    BeamThread st;
-    st.th = st.hit = st.ref = -FLT_MAX;
-    st.known = st.flood = false;
-    st.S = 0.0;
-    constexpr int kStep = NT * kBeamBatch;
-    for (int j = t; j - t < max(cnt, 1); j += 2 * kStep) {
-        load(wb, j + kStep);
-        beam_batch<Tag, VEC>(st, wa, j, P.K, sm);
-        if (j - t + kStep >= cnt) break;
-        load(wa, j + 2 * kStep);
-        beam_batch<Tag, VEC>(st, wb, j + kStep, P.K, sm);
-    }
-    if (xe > -INFINITY || xe != xe) {
-        beam_raise(st, xe);
-        st.S += static_cast<double>(beam_term(xe, st.ref));
-        if (xe >= st.th) {
-            const int at = atomicAdd(&sm.cands, 1);
-            sm.cand[at] = make_key(xe, ie);  // at most 14 of these
+    float ref = fmaxf(peak(a.most(), t0), -FLT_MAX);
+    double S = 0.0;
+    // The terms are summed while the tile's maximum is still on its way; a
+    // maximum far above the reference (rare) takes them again.
+    auto take = [&](const BeamTile<Tag, VEC>& x, int tile) {
+        const float m = peak(x.most(), tile);
+        float s = beam_sum<Tag, VEC>(x.w, ref);
+        if (lane == 0) peaks[tile] = m;
+        if (m > ref + kBeamRaise) {
+            S = beam_carry(S, ref, m);
+            ref = m;
+            s = beam_sum<Tag, VEC>(x.w, ref);
         }
+        S += static_cast<double>(s);
+    };
+    for (int t = t0;;) {
+        take(a, t);
+        if (++t >= t1) break;
+        a.load(row, cut, t);
     }
-    // one reference for the warp (the threads' are the same but for spikes)
-    const float ref = from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(st.ref)));
-    double S = st.S;
-    if (st.ref != ref && S != 0.0) S *= exp(beam_ref(st.ref) - beam_ref(ref));
+    if (ie >= 0) S += static_cast<double>(beam_term(xe, ref));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(FULL_MASK, S, o);
     if (lane == 0) {
-        sm.S[wp] = S;
-        sm.ref[wp] = ref;
-    }
-    __syncthreads();
-    const int64_t chunk = r * P.cpr + sub;
-    if (wp == 0) {  // and one for the CTA
-        S = lane < NWARPS ? sm.S[lane] : 0.0;
-        const float mine = lane < NWARPS ? sm.ref[lane] : -FLT_MAX;
-        const float R = from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(mine)));
-        if (mine != R && S != 0.0) S *= exp(beam_ref(mine) - beam_ref(R));
-#pragma unroll
-        for (int o = NWARPS / 2; o > 0; o >>= 1) S += __shfl_xor_sync(FULL_MASK, S, o);
-        if (lane == 0) {
-            BeamStat o;
-            o.M = beam_ref(R);
-            o.S = S;
-            P.stats[chunk] = o;
-        }
-    }
-    uint64_t* out = P.keys + chunk * P.K;
-    const int vecs = sm.vecs;
-    bool fits = vecs <= kBeamVecs;
-    if (fits) {
-        for (int i = t; i < vecs; i += NT) {
-            const uint4 w = sm.vec[i];
-            const int e0 = cut.head + (v0 + sm.at[i]) * VEC;
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                const float x = VecOps<Tag, VEC>::elem(w, q);
-                if (x >= st.th) {
-                    const int at = atomicAdd(&sm.cands, 1);
-                    if (at < kBeamCand) sm.cand[at] = make_key(x, e0 + q);
-                }
-            }
-        }
-        __syncthreads();
-        fits = sm.cands <= kBeamCand;
-    }
-    if (fits) {
-        // The keys are distinct: a candidate's rank is its place.
-        const int have = sm.cands;
-        for (int i = t; i < have; i += NT) {
-            const uint64_t key = sm.cand[i];
-            int rank = 0;
-            for (int j = 0; j < have; ++j) rank += sm.cand[j] > key ? 1 : 0;
-            if (rank < P.K) out[rank] = key;
-        }
-        for (int i = have + t; i < P.K; i += NT) out[i] = 0ull;
-    } else {
-        beam_chunk_ties<Tag, VEC>(row, cut, v0, cnt, sub == 0, st.th, P.K, sm, out);
+        BeamStat st;
+        st.M = beam_ref(ref);
+        st.S = S;
+        P.stats[r * P.segs + seg] = st;
     }
 }
 
 // ---------------------------------------------------------------------------
-// The request's merge: a CTA with a warp per beam (8 warps at least).
+// The request's merge.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 32;  // warps of the merge CTA at most (8, 16 or 32)
-constexpr int kMergeKeys = 4;    // keys a thread holds in registers
+constexpr int kMergePeaks = 8;    // tiles whose largest logit a thread holds in registers
+constexpr int kMergeTiles = 512;  // tiles of a request that are ranked in shared memory
+constexpr int kMergeCand = 1024;  // candidates of a request that are ranked in shared memory
 
 struct BeamMergeSmem {
-    double M[kMaxBeams];     // largest logit of the row
+    double M[kMaxBeams];     // near the row's largest logit
     double logS[kMaxBeams];  // log sum exp(l - M)
     double s[kMaxBeams];
     int state[kMaxBeams];    // 0: no candidates, 1: streamed, 2: finished
-    double c[kBeamMerge];
-    uint32_t flat[kBeamMerge];  // w V + token
+    double c[kMergeCand];    // tiles, then candidates
+    uint32_t id[kMergeCand];
+    double tile_c[kMaxBeams];   // the K best tiles
+    uint32_t tile_id[kMaxBeams];
     int pool[32];
-    double red_c[kMergeWarps];
-    uint32_t red_f[kMergeWarps];
-    int cnt;
+    double red_c[NWARPS];
+    uint32_t red_id[NWARPS];
+    int tiles, cands;
 };
 
-// A row's sum from its chunks': 32 chunks at a time, each against the largest
-// reference of the 32.  Warp-collective.
-__device__ __forceinline__ BeamStat beam_row_sum(const BeamStat* p, int n) {
+__device__ __forceinline__ double beam_value(const BeamMergeSmem& sm, int w, float x) {
+    return (sm.s[w] + (static_cast<double>(x) - sm.M[w])) - sm.logS[w];
+}
+
+// Segment i of a row's n.
+__device__ __forceinline__ BeamStat beam_stat(const BeamStat* p, int i, int n) {
+    BeamStat x;
+    x.M = -DBL_MAX;
+    x.S = 0.0;
+    if (i < n) {
+        x.M = __ldcg(&p[i].M);
+        x.S = __ldcg(&p[i].S);
+    }
+    return x;
+}
+
+// A row's sum from its segments': 32 at a time (first: this lane's of the first
+// 32), each against the largest reference of the 32.  Warp-collective.
+__device__ __forceinline__ BeamStat beam_row_sum(const BeamStat* p, int n, BeamStat first) {
     const int lane = threadIdx.x & 31;
     BeamStat acc;
     acc.M = -DBL_MAX;
     acc.S = 0.0;
     for (int i0 = 0; i0 < n; i0 += 32) {
-        double M = -DBL_MAX, S = 0.0;
-        if (i0 + lane < n) {
-            M = __ldcg(&p[i0 + lane].M);
-            S = __ldcg(&p[i0 + lane].S);
-        }
-        double top = S != 0.0 ? fmax(M, acc.M) : acc.M;
+        const BeamStat x = i0 == 0 ? first : beam_stat(p, i0 + lane, n);
+        const double M = x.M;
+        double S = x.S, top = S != 0.0 ? fmax(M, acc.M) : acc.M;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(FULL_MASK, top, o));
         if (S != 0.0 && M != top) S *= exp(M - top);
@@ -499,23 +341,38 @@ __device__ __forceinline__ BeamStat beam_row_sum(const BeamStat* p, int n) {
     return acc;
 }
 
-// c of a key of row w.
-__device__ __forceinline__ double beam_value(const BeamMergeSmem& sm, int w, uint64_t key) {
-    return (sm.s[w] + (static_cast<double>(key_value(key)) - sm.M[w])) - sm.logS[w];
-}
-
-// One candidate of the request: none where state[w] has none.
-struct BeamCandidate {
+// The best (c, id), larger c first and then the lower id, of one per thread.
+// CTA-collective; every thread gets it.
+struct BeamBest {
     double c;
-    uint32_t flat;
-    bool ok;
+    uint32_t id;
 };
-__device__ __forceinline__ BeamCandidate beam_candidate(const BeamMergeSmem& sm, int w, uint64_t key, uint32_t V) {
-    BeamCandidate r;
-    r.ok = key != 0ull && sm.state[w] == 1;
-    r.c = r.ok ? beam_value(sm, w, key) : -INFINITY;
-    r.flat = static_cast<uint32_t>(w) * V + static_cast<uint32_t>(key_index(key));
-    return r;
+__device__ __forceinline__ bool beam_before(double c, uint32_t id, double d, uint32_t jd) {
+    return c > d || (c == d && id < jd);
+}
+__device__ __forceinline__ BeamBest beam_block_best(BeamBest x, BeamMergeSmem& sm) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const double c = __shfl_xor_sync(FULL_MASK, x.c, o);
+        const uint32_t id = __shfl_xor_sync(FULL_MASK, x.id, o);
+        if (beam_before(c, id, x.c, x.id)) {
+            x.c = c;
+            x.id = id;
+        }
+    }
+    if (lane == 0) {
+        sm.red_c[wp] = x.c;
+        sm.red_id[wp] = x.id;
+    }
+    __syncthreads();
+    for (int q = 0; q < NWARPS; ++q)
+        if (beam_before(sm.red_c[q], sm.red_id[q], x.c, x.id)) {
+            x.c = sm.red_c[q];
+            x.id = sm.red_id[q];
+        }
+    __syncthreads();
+    return x;
 }
 
 __device__ __forceinline__ void beam_output(const BeamParams& P, int64_t at, double c, uint32_t flat) {
@@ -524,80 +381,124 @@ __device__ __forceinline__ void beam_output(const BeamParams& P, int64_t at, dou
     P.out_tokens[at] = static_cast<int32_t>(flat % static_cast<uint32_t>(P.V));
 }
 
-// More candidates at the bound than kBeamMerge (runs of equal values over many
-// chunks): the best below the last one found, K times.  CTA-collective.
-__device__ __noinline__ void beam_merge_ties(const BeamParams& P, int64_t b, BeamMergeSmem& sm) {
-    const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, wp = t >> 5;
-    const uint32_t V = static_cast<uint32_t>(P.V);
-    const int row_keys = P.cpr * P.K, total = P.W * row_keys;
-    const uint64_t* keys = P.keys + b * total;
-    double lc = INFINITY;
-    uint32_t lf = 0u;
+// The K best tiles of more than kMergeTiles at the bound (runs of equal
+// values): the best one behind the last one found, K times.
+__device__ __noinline__ int beam_many_tiles(const BeamParams& P, const float* peaks, BeamMergeSmem& sm) {
+    const int total = P.W * P.tiles;
+    BeamBest last = {INFINITY, 0u};
     for (int i = 0; i < P.K; ++i) {
-        double bc = -INFINITY;
-        uint32_t bf = 0xffffffffu;
-        auto offer = [&](double c, uint32_t f) {
-            const bool below = c < lc || (c == lc && f > lf);
-            if (below && (c > bc || (c == bc && f < bf))) {
-                bc = c;
-                bf = f;
-            }
-        };
-        for (int w = t; w < P.W; w += nt)
-            if (sm.state[w] == 2) offer(sm.s[w], static_cast<uint32_t>(w) * V + static_cast<uint32_t>(P.eos));
-        for (int j = t; j < total; j += nt) {
-            const BeamCandidate q = beam_candidate(sm, j / row_keys, __ldcg(&keys[j]), V);
-            if (q.ok) offer(q.c, q.flat);
+        BeamBest best = {-INFINITY, 0xffffffffu};
+        for (int j = threadIdx.x; j < total; j += NT) {
+            const int w = j / P.tiles;
+            const float m = sm.state[w] == 1 ? __ldcg(&peaks[j]) : -INFINITY;
+            if (!(m > -INFINITY)) continue;
+            const double c = beam_value(sm, w, m);
+            if (beam_before(last.c, last.id, c, j) && beam_before(c, j, best.c, best.id)) best = {c, static_cast<uint32_t>(j)};
         }
-        auto join = [&](double c, uint32_t f) {
-            if (c > bc || (c == bc && f < bf)) {
-                bc = c;
-                bf = f;
+        last = beam_block_best(best, sm);
+        if (last.id == 0xffffffffu) return i;
+        if (threadIdx.x == 0) {
+            sm.tile_c[i] = last.c;
+            sm.tile_id[i] = last.id;
+        }
+    }
+    return P.K;
+}
+
+// Every element of the n best tiles with a value of at least `bound`, and the
+// finished beams: f(c, w V + token).  A warp per tile.
+template <class Tag, int VEC, class F>
+__device__ __forceinline__ void beam_visit(const BeamParams& P, int64_t b, int n, double bound, const BeamMergeSmem& sm, F f) {
+    using Elem = typename Tag::storage;
+    const int wp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t V = static_cast<uint32_t>(P.V);
+    struct Place {
+        const Elem* row;
+        RowCut cut;
+        int w, tile, ie;
+        float xe;
+    };
+    auto load = [&](int i, BeamTile<Tag, VEC>& a) {
+        Place p;
+        p.w = static_cast<int>(sm.tile_id[i]) / P.tiles;
+        p.tile = static_cast<int>(sm.tile_id[i]) - p.w * P.tiles;
+        p.row = static_cast<const Elem*>(P.logits) + (b * P.W + p.w) * P.row_stride;
+        p.cut = cut_row<Tag, VEC>(p.row, P.V);
+        a.load(p.row, p.cut, p.tile);
+        p.xe = beam_end<Tag>(p.row, p.cut, P.V, p.tile == 0, p.tile == P.tiles - 1, p.ie);
+        return p;
+    };
+    auto look = [&](const Place& p, const BeamTile<Tag, VEC>& a) {
+        const int w = p.w;
+        // A logit below this has a value below the bound (the margin covers the
+        // rounding of the fp64 sums); what passes is compared in fp64.
+        const double at = (bound - sm.s[w]) + sm.logS[w] + sm.M[w];
+        const double slack = 1e-12 * (fabs(bound) + fabs(sm.s[w]) + fabs(sm.logS[w]) + fabs(sm.M[w]));
+        const float low = bound > -INFINITY ? fmaxf(__double2float_rd(at - slack), -FLT_MAX) : -FLT_MAX;
+        auto offer = [&](float x, int e) {
+            if (x >= low) {
+                const double c = beam_value(sm, w, x);
+                if (c >= bound) f(c, static_cast<uint32_t>(w) * V + static_cast<uint32_t>(e));
             }
         };
+        if (p.ie >= 0) offer(p.xe, p.ie);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double c = __shfl_xor_sync(FULL_MASK, bc, o);
-            const uint32_t f = __shfl_xor_sync(FULL_MASK, bf, o);
-            join(c, f);
+        for (int u = 0; u < kTileU; ++u) {
+            if (!(VecOps<Tag, VEC>::vmax(a.w[u]) >= low)) continue;
+            const int e0 = p.cut.head + (p.tile * kTileVecs + u * 32 + lane) * VEC;
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) offer(VecOps<Tag, VEC>::elem(a.w[u], q), e0 + q);
         }
-        if (lane == 0) {
-            sm.red_c[wp] = bc;
-            sm.red_f[wp] = bf;
-        }
-        __syncthreads();
-        for (int q = 0; q < (nt >> 5); ++q) join(sm.red_c[q], sm.red_f[q]);
-        __syncthreads();
-        lc = bc;
-        lf = bf;
-        if (t == 0) beam_output(P, b * P.K + i, bc, bf);
+    };
+    for (int i = wp; i < n; i += 2 * NWARPS) {  // two tiles on their way
+        BeamTile<Tag, VEC> x, y;
+        const Place p = load(i, x);
+        Place q = p;
+        if (i + NWARPS < n) q = load(i + NWARPS, y);
+        look(p, x);
+        if (i + NWARPS < n) look(q, y);
+    }
+    for (int w = threadIdx.x; w < P.W; w += NT)
+        if (sm.state[w] == 2 && sm.s[w] >= bound)
+            f(sm.s[w], static_cast<uint32_t>(w) * V + static_cast<uint32_t>(P.eos));
+}
+
+// The outputs of more than kMergeCand candidates: the best one behind the last
+// one found, K times.
+template <class Tag, int VEC>
+__device__ __noinline__ void beam_many_candidates(const BeamParams& P, int64_t b, int n, double bound, BeamMergeSmem& sm) {
+    BeamBest last = {INFINITY, 0u};
+    for (int i = 0; i < P.K; ++i) {
+        BeamBest best = {-INFINITY, 0xffffffffu};
+        beam_visit<Tag, VEC>(P, b, n, bound, sm, [&](double c, uint32_t id) {
+            if (beam_before(last.c, last.id, c, id) && beam_before(c, id, best.c, best.id)) best = {c, id};
+        });
+        last = beam_block_best(best, sm);
+        if (threadIdx.x == 0) beam_output(P, b * P.K + i, last.c, last.id);
     }
 }
 
-__global__ void __launch_bounds__(32 * kMergeWarps) beam_merge_kernel(const BeamParams P) {
-    __shared__ BeamMergeSmem sm;
-    const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, wp = t >> 5, nw = nt >> 5;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t b = blockIdx.x;
-    const int K = P.K, cpr = P.cpr;
-    const uint32_t V = static_cast<uint32_t>(P.V);
-    const int row_keys = cpr * K, total = P.W * row_keys;
-    const uint64_t* keys = P.keys + b * total;
-    // Key j of this thread: every warp gets keys of all rows, chunks and ranks,
-    // so that the warps' largest are the request's largest.
-    auto at = [&](int j) { return j * nt + lane * nw + ((wp + lane) & (nw - 1)); };
-    // The keys' loads go out before the rows' sums are merged.  Rows that were
-    // not streamed hold nothing; their keys are read but not used.
-    uint64_t kk[kMergeKeys];
+// CTA-collective.
+template <class Tag, int VEC>
+__device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamMergeSmem& sm) {
+    const int t = threadIdx.x, lane = t & 31, wp = t >> 5;
+    const int K = P.K, total = P.W * P.tiles;
+    const float* peaks = P.peaks + b * total;
+    // Tile j of this thread: every warp gets tiles of all rows, so that the
+    // warps' best are the request's best.  The loads go out before the rows'
+    // sums are merged; rows that were not streamed hold nothing, what is read
+    // there is not used.
+    auto nth = [&](int j) { return j * NT + lane * NWARPS + ((wp + lane) & (NWARPS - 1)); };
+    const BeamStat first = beam_stat(P.stats + (b * P.W + min(wp, P.W - 1)) * P.segs, lane, P.segs);
+    float m[kMergePeaks];
 #pragma unroll
-    for (int j = 0; j < kMergeKeys; ++j) {
-        const int i = at(j);
-        kk[j] = i < total ? __ldcg(&keys[i]) : 0ull;
+    for (int j = 0; j < kMergePeaks; ++j) {
+        const int i = nth(j);
+        m[j] = i < total ? __ldcg(&peaks[i]) : -INFINITY;
     }
-    if (t == 0) sm.cnt = 0;
+    if (t == 0) sm.tiles = sm.cands = 0;
     int bad = 0;
-    for (int w = wp; w < P.W; w += nw) {
+    for (int w = wp; w < P.W; w += NWARPS) {
         const int64_t r = b * P.W + w;
         const float s = __ldg(&P.scores[r]);
         const bool fin = P.finished != nullptr && __ldg(&P.finished[r]) != 0;
@@ -609,7 +510,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) beam_merge_kernel(const Beam
             if (fin) {
                 state = 2;
             } else {
-                const BeamStat a = beam_row_sum(P.stats + r * cpr, cpr);
+                const BeamStat* p = P.stats + r * P.segs;
+                const BeamStat a = beam_row_sum(p, P.segs, w == wp ? first : beam_stat(p, lane, P.segs));
                 if (!(a.S <= DBL_MAX)) {
                     bad = 1;  // a NaN or +inf logit
                 } else if (a.S > 0.0) {
@@ -627,66 +529,140 @@ __global__ void __launch_bounds__(32 * kMergeWarps) beam_merge_kernel(const Beam
         }
     }
     if (__syncthreads_or(bad)) {
-        for (int i = t; i < K; i += nt) {
+        for (int i = t; i < K; i += NT) {
             P.out_scores[b * K + i] = __uint_as_float(0x7fc00000u);
             P.out_parents[b * K + i] = -1;
             P.out_tokens[b * K + i] = -1;
         }
         return;
     }
-    // A bound that K candidates reach, from each thread's best (rounded down to
+    // The tiles' values, and a bound that K of them reach: the K-th largest of
+    // the 32 that the warps' 32 / NWARPS largest lanes make up (rounded down to
     // fp32).
-    BeamCandidate q[kMergeKeys];
-    double best = -INFINITY;
+    auto value = [&](int i, float x) {
+        const int w = i / P.tiles;
+        return x > -INFINITY && sm.state[w] == 1 ? beam_value(sm, w, x) : -INFINITY;
+    };
+    double c[kMergePeaks], best = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kMergeKeys; ++j) {
-        const int i = at(j);
-        q[j] = beam_candidate(sm, i < total ? i / row_keys : 0, kk[j], V);
-        best = fmax(best, q[j].c);
+    for (int j = 0; j < kMergePeaks; ++j) {
+        const int i = nth(j);
+        c[j] = i < total ? value(i, m[j]) : -INFINITY;
+        best = fmax(best, c[j]);
     }
-    for (int j = kMergeKeys; j * nt < total; ++j) {
-        const int i = at(j);
-        if (i < total) best = fmax(best, beam_candidate(sm, i / row_keys, __ldcg(&keys[i]), V).c);
+    for (int j = kMergePeaks; j * NT < total; ++j) {
+        const int i = nth(j);
+        if (i < total) best = fmax(best, value(i, __ldcg(&peaks[i])));
     }
-    const int kth = cta_kth(ord_i32(__double2float_rd(best)), K, nw, sm.pool).x;
-    const double bound = kth == INT_MIN ? -INFINITY : static_cast<double>(from_ord_i32(kth));
-    auto keep = [&](double c, uint32_t flat) {
-        const int place = atomicAdd(&sm.cnt, 1);
-        if (place < kBeamMerge) {
-            sm.c[place] = c;
-            sm.flat[place] = flat;
+    int o = ord_i32(__double2float_rd(best)), mine = INT_MIN;
+    for (int i = 0; i < 32 / NWARPS; ++i) {
+        const int x = __reduce_max_sync(FULL_MASK, o);
+        if (lane == i) mine = x;
+        const unsigned who = __ballot_sync(FULL_MASK, o == x);
+        if (lane == __ffs(who) - 1) o = INT_MIN;
+    }
+    if (lane < 32 / NWARPS) sm.pool[wp * (32 / NWARPS) + lane] = mine;
+    __syncthreads();
+    const int kth = warp_kth(sm.pool[lane], K);
+    const double floor = kth == INT_MIN ? -INFINITY : static_cast<double>(from_ord_i32(kth));
+    auto keep = [&](double v, int i) {
+        if (!(v >= floor && v > -INFINITY)) return;
+        const int at = atomicAdd(&sm.tiles, 1);
+        if (at < kMergeTiles) {
+            sm.c[at] = v;
+            sm.id[at] = static_cast<uint32_t>(i);
         }
     };
-    for (int w = t; w < P.W; w += nt)
-        if (sm.state[w] == 2 && sm.s[w] >= bound) keep(sm.s[w], static_cast<uint32_t>(w) * V + static_cast<uint32_t>(P.eos));
 #pragma unroll
-    for (int j = 0; j < kMergeKeys; ++j)
-        if (q[j].ok && q[j].c >= bound) keep(q[j].c, q[j].flat);
-    for (int j = kMergeKeys; j * nt < total; ++j) {
-        const int i = at(j);
-        if (i >= total) continue;
-        const BeamCandidate x = beam_candidate(sm, i / row_keys, __ldcg(&keys[i]), V);
-        if (x.ok && x.c >= bound) keep(x.c, x.flat);
+    for (int j = 0; j < kMergePeaks; ++j) keep(c[j], nth(j));
+    for (int j = kMergePeaks; j * NT < total; ++j) {
+        const int i = nth(j);
+        if (i < total) keep(value(i, __ldcg(&peaks[i])), i);
     }
     __syncthreads();
-    const int have = sm.cnt;
-    if (have > kBeamMerge) {
-        beam_merge_ties(P, b, sm);
+    // The K best tiles, a tile's rank being its place.
+    const int have = sm.tiles;
+    int n = min(have, K);
+    if (have <= kMergeTiles) {
+        for (int i = t; i < have; i += NT) {
+            const double v = sm.c[i];
+            const uint32_t id = sm.id[i];
+            int rank = 0;
+            for (int j = 0; j < have; ++j) rank += beam_before(sm.c[j], sm.id[j], v, id) ? 1 : 0;
+            if (rank < K) {
+                sm.tile_c[rank] = v;
+                sm.tile_id[rank] = id;
+            }
+        }
+    } else {
+        n = beam_many_tiles(P, peaks, sm);
+    }
+    __syncthreads();
+    const double bound = n == K ? sm.tile_c[K - 1] : -INFINITY;
+    beam_visit<Tag, VEC>(P, b, n, bound, sm, [&](double v, uint32_t id) {
+        const int at = atomicAdd(&sm.cands, 1);
+        if (at < kMergeCand) {
+            sm.c[at] = v;
+            sm.id[at] = id;
+        }
+    });
+    __syncthreads();
+    const int cands = sm.cands;
+    if (cands > kMergeCand) {
+        beam_many_candidates<Tag, VEC>(P, b, n, bound, sm);
         return;
     }
-    // The candidates differ in w V + token: a candidate's rank is its place.
-    for (int i = t; i < have; i += nt) {
-        const double c = sm.c[i];
-        const uint32_t f = sm.flat[i];
+    for (int i = t; i < cands; i += NT) {
+        const double v = sm.c[i];
+        const uint32_t id = sm.id[i];
         int rank = 0;
-        for (int j = 0; j < have; ++j) rank += sm.c[j] > c || (sm.c[j] == c && sm.flat[j] < f) ? 1 : 0;
-        if (rank < K) beam_output(P, b * K + rank, c, f);
+        for (int j = 0; j < cands; ++j) rank += beam_before(sm.c[j], sm.id[j], v, id) ? 1 : 0;
+        if (rank < K) beam_output(P, b * K + rank, v, id);
     }
-    for (int i = have + t; i < K; i += nt) {
+    for (int i = cands + t; i < K; i += NT) {
         P.out_scores[b * K + i] = -INFINITY;
         P.out_parents[b * K + i] = -1;
         P.out_tokens[b * K + i] = -1;
     }
+}
+
+// Rows of many tiles: a warp per segment, then a CTA per request.  The second
+// kernel's launch overlaps the first one's end.  (One kernel whose last CTA
+// per request merges, found by an atomic ticket, is slower: every CTA then
+// waits for a memory fence and the ticket before it leaves its place, 38 us
+// against 33.5 us at 64 x 8 rows of 128256 bf16.)
+template <class Tag, int VEC>
+__global__ void __launch_bounds__(NT, 5) beam_pass_kernel(const BeamParams P) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const unsigned unit = blockIdx.x * NWARPS + (threadIdx.x >> 5);
+    const unsigned r = unit / static_cast<unsigned>(P.segs);
+    if (r >= static_cast<unsigned>(P.B * P.W) || !beam_streams(P, r)) return;  // warp-uniform; no CTA barrier below
+    beam_stream<Tag, VEC>(P, r, static_cast<int>(unit - r * static_cast<unsigned>(P.segs)));
+}
+
+template <class Tag, int VEC>
+__global__ void __launch_bounds__(NT, 2) beam_merge_kernel(const BeamParams P) {
+    __shared__ BeamMergeSmem sm;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    beam_merge<Tag, VEC>(P, blockIdx.x, sm);
+}
+
+// Requests of at most kSmallTiles tiles: one CTA does both, in one launch.
+constexpr int kSmallTiles = 32;
+template <class Tag, int VEC>
+__global__ void __launch_bounds__(NT, 2) beam_small_kernel(const BeamParams P) {
+    __shared__ BeamMergeSmem sm;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t b = blockIdx.x;
+    for (int unit = threadIdx.x >> 5; unit < P.W * P.segs; unit += NWARPS) {
+        const int w = unit / P.segs;
+        if (beam_streams(P, b * P.W + w)) beam_stream<Tag, VEC>(P, b * P.W + w, unit - w * P.segs);
+    }
+    __syncthreads();
+    beam_merge<Tag, VEC>(P, b, sm);
 }
 
 }  // namespace specdec

@@ -9,11 +9,16 @@
 // from a ring of free pages in request order, and those of released requests
 // go back to it.
 //
-// plan_tables_kernel: lengths, page counts, prefix sums of the pages asked
-// for, the tables' new entries and the ring.  plan_slots_kernel: positions
-// and slots of the rows.
+// plan_tables_kernel: lengths, page counts, prefix sums of the pages asked for
+// and returned, the tables' new entries and the ring.  One cluster of up to 8
+// CTAs, a thread per request (several beyond 8192): the CTAs' totals go
+// through distributed shared memory, so the whole batch is scanned in one
+// launch.  Bound by the latency of its few dependent reads, not by bytes.
+// A batch that one CTA holds and whose rows are few gets its positions and
+// slots in the same launch; otherwise plan_slots_kernel writes them.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>
@@ -24,6 +29,8 @@
 namespace specdec {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCtas = 8;         // CTAs of the cluster at most (the portable cluster size)
+constexpr int kPlanFusedRows = 8192; // rows that plan_tables_kernel maps itself (one CTA)
 
 struct PlanParams {
     const int32_t* seq_lens;    // [B]
@@ -69,152 +76,240 @@ __device__ __forceinline__ PlanRows plan_rows(const PlanParams& P, int64_t b) {
 struct PlanNeed {
     int64_t len;
     int held, grow, back;
+    bool gone;
 };
-__device__ __forceinline__ PlanNeed plan_need(const PlanParams& P, int64_t b) {
+__device__ __forceinline__ PlanNeed plan_need(const PlanParams& P, int64_t b, const PlanRows& rows) {
     PlanNeed q;
-    const int h = __ldg(&P.held[b]);
+    const int h = P.held[b], l = P.seq_lens[b];  // plain loads: the outputs may be the same arrays
+    const int a = P.accept_len != nullptr ? __ldg(&P.accept_len[b]) : -1;
+    q.gone = P.release != nullptr && __ldg(&P.release[b]) != 0;
     q.held = h < 0 ? 0 : (h < P.max_blocks ? h : P.max_blocks);
     q.grow = q.back = 0;
     q.len = 0;
-    if (P.release != nullptr && __ldg(&P.release[b]) != 0) {
+    if (q.gone) {
         q.back = q.held;
         return q;
     }
-    const int l = P.seq_lens[b];
     q.len = l < 0 ? 0 : l;
-    if (P.accept_len != nullptr) {
-        const int a = __ldg(&P.accept_len[b]);
-        if (a >= 0) q.len += static_cast<int64_t>(a) + 1;
-    }
+    if (a >= 0) q.len += static_cast<int64_t>(a) + 1;
     if (q.len > INT_MAX) q.len = INT_MAX;
-    const int64_t n = plan_rows(P, b).n;
-    const int64_t need = n > 0 ? (q.len + n + P.block_size - 1) / P.block_size : 0;
-    if (need <= P.max_blocks && need > q.held) q.grow = static_cast<int>(need) - q.held;
+    // len + n + block_size stays below 2^32
+    const unsigned need = rows.n > 0 ? (static_cast<unsigned>(q.len + rows.n - 1)) / static_cast<unsigned>(P.block_size) + 1u : 0u;
+    if (need <= static_cast<unsigned>(P.max_blocks) && static_cast<int>(need) > q.held) q.grow = static_cast<int>(need) - q.held;
     return q;
 }
 
-// CTA-wide exclusive prefix sums of two counts in thread order.
+// Prefix sums of pages asked for and returned.
 struct PlanScan {
     int64_t grow, back;
 };
-__device__ __forceinline__ PlanScan plan_scan(PlanScan v, PlanScan* red, PlanScan* total) {
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    PlanScan incl = v;
+__device__ __forceinline__ PlanScan warp_inclusive(PlanScan v, bool backs) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t g = __shfl_up_sync(FULL_MASK, incl.grow, o), k = __shfl_up_sync(FULL_MASK, incl.back, o);
-        if (lane >= o) {
-            incl.grow += g;
-            incl.back += k;
+        const int64_t g = __shfl_up_sync(FULL_MASK, v.grow, o);
+        if (lane >= o) v.grow += g;
+    }
+    if (backs) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t k = __shfl_up_sync(FULL_MASK, v.back, o);
+            if (lane >= o) v.back += k;
         }
     }
-    if (lane == 31) red[wp] = incl;
-    __syncthreads();
-    PlanScan before = {0, 0}, all = {0, 0};
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < wp) {
-            before.grow += red[w].grow;
-            before.back += red[w].back;
-        }
-        all.grow += red[w].grow;
-        all.back += red[w].back;
-    }
-    __syncthreads();
-    *total = all;
-    PlanScan ex;
-    ex.grow = before.grow + incl.grow - v.grow;
-    ex.back = before.back + incl.back - v.back;
-    return ex;
+    return v;
 }
 
-__device__ __forceinline__ int64_t wrap(int64_t x, int64_t cap) { return x % cap; }
+// Slot of position p of a request that holds `held` pages.
+__device__ __forceinline__ int64_t plan_slot(const PlanParams& P, const int32_t* table, unsigned p, int held) {
+    const unsigned page = p / static_cast<unsigned>(P.block_size);
+    if (page >= static_cast<unsigned>(held)) return -1;
+    const int block = __ldcg(&table[page]);
+    return block >= 0 ? static_cast<int64_t>(block) * P.block_size + (p - page * static_cast<unsigned>(P.block_size)) : -1;
+}
 
+// One request's page moves: new table entries from the ring's head, or the
+// pages it held back behind the tail.  Indexes stay below 2 capacities.
+struct PlanMove {
+    int64_t b, first, ret;
+    int got, held;
+};
+__device__ __forceinline__ void plan_move(const PlanParams& P, const PlanMove& m, int64_t head, int64_t count, int i0,
+                                          int step) {
+    int32_t* row = P.tables + m.b * P.table_stride;
+    if (m.got > 0) {
+        for (int i = i0; i < m.got; i += step) {
+            int64_t at = head + m.first + i;
+            if (at >= P.capacity) at -= P.capacity;
+            row[m.held + i] = P.ring[at];
+        }
+    } else {
+        for (int i = i0; i < m.held && count + m.ret + i < P.capacity; i += step) {
+            int64_t at = head + count + m.ret + i;
+            if (at >= P.capacity) at -= P.capacity;
+            P.ring[at] = row[i];
+        }
+    }
+}
+
+constexpr int kPlanOwn = 4;  // pages that a thread moves by itself; longer moves are shared by its warp
+
+struct PlanSmem {
+    PlanScan warp[kPlanThreads / 32];
+    PlanScan cta[kPlanCtas];        // written by the cluster's CTAs
+    unsigned long long taken[kPlanCtas];
+    unsigned long long most;
+    // one CTA that also maps the rows
+    unsigned len[kPlanThreads];
+    int held[kPlanThreads];         // -1: released
+    int64_t row0[kPlanThreads];
+    uint16_t request[kPlanFusedRows];
+};
+
+template <bool FUSED>
 __global__ void __launch_bounds__(kPlanThreads) plan_tables_kernel(const PlanParams P) {
-    __shared__ PlanScan red[kPlanThreads / 32];
-    __shared__ int64_t taken_s;
-    const int lane = threadIdx.x & 31;
+    namespace cg = cooperative_groups;
+    __shared__ PlanSmem sm;
+    const int t = threadIdx.x, lane = t & 31, wp = t >> 5;
+    const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster
     grid_dependency_wait();
     grid_launch_dependents();
+    const int per = (P.B + ctas * kPlanThreads - 1) / (ctas * kPlanThreads);  // requests of a thread, consecutive
+    const int64_t b0 = (static_cast<int64_t>(rank) * kPlanThreads + t) * per;
+    const bool backs = P.release != nullptr;
     int64_t head = P.ring_state[0], count = P.ring_state[1];
+    const int64_t rows = FUSED ? (P.offsets == nullptr ? static_cast<int64_t>(P.B) * (P.k + 1) : P.B + P.total) : 0;
+    if (FUSED && P.offsets != nullptr)
+        for (int i = t; i < rows; i += kPlanThreads) sm.request[i] = 0xffffu;
+    PlanScan mine = {0, 0};
+    PlanNeed q = {0, 0, 0, 0, false};
+    PlanRows pr = {0, 0};
+    for (int i = 0; i < per; ++i)
+        if (b0 + i < P.B) {
+            pr = plan_rows(P, b0 + i);
+            q = plan_need(P, b0 + i, pr);
+            mine.grow += q.grow;
+            mine.back += q.back;
+        }
     if (head < 0 || head >= P.capacity) head = 0;
     if (count < 0) count = 0;
     if (count > P.capacity) count = P.capacity;
-    if (threadIdx.x == 0) taken_s = 0;
+    if (t == 0) sm.most = 0ull;
+    PlanScan incl = warp_inclusive(mine, backs);
+    if (lane == 31) sm.warp[wp] = incl;
     __syncthreads();
-    PlanScan carry = {0, 0};
-    int64_t most = 0;  // pages granted up to the last request of this thread that got its pages
-    for (int64_t b0 = 0; b0 < P.B; b0 += kPlanThreads) {
-        const int64_t b = b0 + threadIdx.x;
-        PlanNeed q = {0, 0, 0, 0};
-        if (b < P.B) q = plan_need(P, b);
-        PlanScan v = {q.grow, q.back}, total;
-        const PlanScan ex = plan_scan(v, red, &total);
-        const int64_t first = carry.grow + ex.grow, ret = carry.back + ex.back;
-        carry.grow += total.grow;
-        carry.back += total.back;
-        int got = first + q.grow <= count ? q.grow : 0;
-        if (got > 0) most = first + got;
-        if (b < P.B) {
-            P.seq_out[b] = static_cast<int32_t>(q.len);
-            P.held_out[b] = q.back > 0 || (P.release != nullptr && __ldg(&P.release[b]) != 0) ? 0 : q.held + got;
+    PlanScan w = warp_inclusive(sm.warp[lane], backs);  // over the warps, in every warp
+    PlanScan all = {__shfl_sync(FULL_MASK, w.grow, 31), __shfl_sync(FULL_MASK, w.back, 31)};
+    PlanScan before = {__shfl_sync(FULL_MASK, w.grow, (wp + 31) & 31), __shfl_sync(FULL_MASK, w.back, (wp + 31) & 31)};
+    if (wp == 0) before = {0, 0};
+    PlanScan at = {before.grow + incl.grow - mine.grow, before.back + incl.back - mine.back};
+    if (!FUSED && ctas > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
+        if (t < ctas) cluster.map_shared_rank(&sm, t)->cta[rank] = all;
+        cluster.sync();
+        PlanScan total = {0, 0};
+        for (int i = 0; i < ctas; ++i) {
+            const PlanScan c = sm.cta[i];
+            if (i < rank) {
+                at.grow += c.grow;
+                at.back += c.back;
+            }
+            total.grow += c.grow;
+            total.back += c.back;
         }
-        // New table entries and returned pages, a warp at a time: the lanes of
-        // the warp share each request's pages.
-        const int moves = got > 0 ? got : q.back;
-        for (unsigned m = __ballot_sync(FULL_MASK, moves > 0); m != 0u; m &= m - 1u) {
-            const int l = __ffs(m) - 1;
-            const int64_t rb = __shfl_sync(FULL_MASK, b, l);
-            const int g = __shfl_sync(FULL_MASK, got, l), h = __shfl_sync(FULL_MASK, q.held, l);
-            const int64_t f = __shfl_sync(FULL_MASK, first, l), rt = __shfl_sync(FULL_MASK, ret, l);
-            int32_t* row = P.tables + rb * P.table_stride;
-            if (g > 0) {
-                for (int i = lane; i < g; i += 32) row[h + i] = P.ring[wrap(head + f + i, P.capacity)];
-            } else {
-                for (int i = lane; i < h; i += 32)
-                    if (count + rt + i < P.capacity) P.ring[wrap(head + count + rt + i, P.capacity)] = row[i];
+        all = total;
+    }
+    // Requests whose pages the ring holds get them.
+    int64_t most = 0;  // pages taken up to this thread's last such request
+    for (int i = 0; i < per; ++i) {
+        const int64_t b = b0 + i;
+        PlanMove m = {b, at.grow, at.back, 0, 0};
+        if (b < P.B) {
+            if (per > 1) {
+                pr = plan_rows(P, b);
+                q = plan_need(P, b, pr);
+            }
+            if (at.grow + q.grow <= count) m.got = q.grow;
+            m.held = q.held;
+            if (m.got > 0) most = at.grow + m.got;
+            at.grow += q.grow;
+            at.back += q.back;
+            const int held = q.gone ? 0 : q.held + m.got;
+            P.seq_out[b] = static_cast<int32_t>(q.len);
+            P.held_out[b] = held;
+            if (FUSED) {
+                sm.len[t] = static_cast<unsigned>(q.len);
+                sm.held[t] = q.gone ? -1 : held;
+                sm.row0[t] = pr.row0;
+                if (P.offsets != nullptr)
+                    for (int64_t j = pr.row0; j < pr.row0 + pr.n; ++j) sm.request[j] = static_cast<uint16_t>(t);
             }
         }
-    }
-    if (most > 0) atomicMax(reinterpret_cast<unsigned long long*>(&taken_s), static_cast<unsigned long long>(most));
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const int64_t taken = taken_s;
-        const int64_t back = carry.back < P.capacity - count ? carry.back : P.capacity - count;
-        P.ring_out[0] = static_cast<int32_t>(wrap(head + taken, P.capacity));
-        P.ring_out[1] = static_cast<int32_t>(count - taken + back);
-    }
-}
-
-// Slots of one request's rows first, first + step, ...
-__device__ __forceinline__ void write_slots(const PlanParams& P, int64_t b, int64_t first, int64_t end, int64_t step) {
-    const PlanRows r = plan_rows(P, b);
-    const bool gone = P.release != nullptr && __ldg(&P.release[b]) != 0;
-    const int64_t len = __ldcg(&P.seq_out[b]);
-    const int held = __ldcg(&P.held_out[b]);
-    const int32_t* row = P.tables + b * P.table_stride;
-    if (end > r.n) end = r.n;
-    for (int64_t j = first; j < end; j += step) {
-        const int64_t p = len + j;
-        const int64_t page = p / P.block_size;
-        int64_t slot = -1;
-        if (!gone && page < held) {
-            const int block = __ldcg(&row[page]);
-            if (block >= 0) slot = static_cast<int64_t>(block) * P.block_size + (p - page * P.block_size);
+        const int pages = b < P.B ? (m.got > 0 ? m.got : q.back) : 0;
+        if (pages > 0 && pages <= kPlanOwn) plan_move(P, m, head, count, 0, 1);
+        for (unsigned long_ones = __ballot_sync(FULL_MASK, pages > kPlanOwn); long_ones != 0u; long_ones &= long_ones - 1u) {
+            const int l = __ffs(long_ones) - 1;
+            PlanMove x;
+            x.b = __shfl_sync(FULL_MASK, m.b, l);
+            x.first = __shfl_sync(FULL_MASK, m.first, l);
+            x.ret = __shfl_sync(FULL_MASK, m.ret, l);
+            x.got = __shfl_sync(FULL_MASK, m.got, l);
+            x.held = __shfl_sync(FULL_MASK, m.held, l);
+            plan_move(P, x, head, count, lane, 32);
         }
-        P.positions[r.row0 + j] = gone ? -1 : p;
-        P.slots[r.row0 + j] = slot;
+    }
+    // The ring after this call: what the last granted request took up to.
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(FULL_MASK, most, o));
+    if (lane == 0 && most > 0) atomicMax(&sm.most, static_cast<unsigned long long>(most));
+    __syncthreads();
+    unsigned long long taken = sm.most;
+    if (!FUSED && ctas > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
+        if (t == 0) cluster.map_shared_rank(&sm, 0)->taken[rank] = taken;
+        cluster.sync();  // also: every CTA has read the ring's state
+        if (rank == 0)
+            for (int i = 0; i < ctas; ++i) taken = max(taken, sm.taken[i]);
+    }
+    if (rank == 0 && t == 0) {
+        const int64_t back = all.back < P.capacity - count ? all.back : P.capacity - count;
+        int64_t h = head + static_cast<int64_t>(taken);
+        if (h >= P.capacity) h -= P.capacity;
+        P.ring_out[0] = static_cast<int32_t>(h);
+        P.ring_out[1] = static_cast<int32_t>(count - static_cast<int64_t>(taken) + back);
+    }
+    if (FUSED) {  // a thread per row; the tables' entries were written by this CTA before the barrier
+        for (int i = t; i < rows; i += kPlanThreads) {
+            const unsigned b = P.offsets == nullptr ? static_cast<unsigned>(i) / static_cast<unsigned>(P.k + 1) : sm.request[i];
+            if (b == 0xffffu) continue;
+            const int held = sm.held[b];
+            const unsigned p = sm.len[b] + static_cast<unsigned>(i - sm.row0[b]);
+            P.positions[i] = held < 0 ? -1 : static_cast<int64_t>(p);
+            P.slots[i] = held < 0 ? -1 : plan_slot(P, P.tables + b * P.table_stride, p, held);
+        }
     }
 }
 
 constexpr int kSlotTile = 1024;  // rows of a request per warp
 
+// A warp per request and tile of its rows.
 __global__ void __launch_bounds__(NT) plan_slots_kernel(const PlanParams P) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t b = static_cast<int64_t>(blockIdx.x) * NWARPS + (threadIdx.x >> 5);
     if (b >= P.B) return;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kSlotTile;
-    write_slots(P, b, r0 + (threadIdx.x & 31), r0 + kSlotTile, 32);
+    const int lane = threadIdx.x & 31;
+    const int64_t first = static_cast<int64_t>(blockIdx.y) * kSlotTile;
+    const PlanRows r = plan_rows(P, b);
+    const bool gone = P.release != nullptr && __ldg(&P.release[b]) != 0;
+    const unsigned len = static_cast<unsigned>(__ldcg(&P.seq_out[b]));
+    const int held = __ldcg(&P.held_out[b]);
+    const int64_t end = min(r.n, first + kSlotTile);
+    for (int64_t j = first + lane; j < end; j += 32) {
+        const unsigned p = len + static_cast<unsigned>(j);
+        P.positions[r.row0 + j] = gone ? -1 : static_cast<int64_t>(p);
+        P.slots[r.row0 + j] = gone ? -1 : plan_slot(P, P.tables + b * P.table_stride, p, held);
+    }
 }
 
 }  // namespace specdec

@@ -12,7 +12,6 @@
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
-#include <stdlib.h>
 
 #include <atomic>
 
@@ -216,47 +215,63 @@ void fill_common(Pass1Params& P, const void* logits, int64_t row_stride, int V, 
 namespace specdec {
 namespace {
 
-// Beam selection: the chunks' statistics and best keys, behind the fixed area
-// (which it does not touch).
-#ifndef BEAM_CHUNK
-#define BEAM_CHUNK 4096
-#endif
-int beam_chunk_vecs(int64_t rows, int nv) {
-    static const char* e = getenv("BEAM_CHUNK");
-    if (e) return atoi(e);
-    (void)rows;
-    (void)nv;
-    return BEAM_CHUNK;
-}
-
+// Beam selection: the segments' sums and the tiles' largest logits, behind the
+// fixed area (which it does not touch).
 struct BeamLayout {
-    int cpr = 0;
-    size_t stats = 0, keys = 0, total = 0;
+    int tiles = 0, seg_tiles = 0, segs = 0;
+    size_t stats = 0, peaks = 0, total = 0;
 };
 
-BeamLayout make_beam_layout(int B, int W, int K, int V, specdec_dtype dtype) {
+BeamLayout make_beam_layout(int B, int W, int V, specdec_dtype dtype) {
     BeamLayout L;
-    const int ve = vec_elems(dtype);
-    const int nv = V / ve;
-    const int chunk = beam_chunk_vecs(static_cast<int64_t>(B) * W, nv);
-    L.cpr = nv > chunk ? (nv + chunk - 1) / chunk : 1;
-    const size_t chunks = static_cast<size_t>(B) * static_cast<size_t>(W) * static_cast<size_t>(L.cpr);
+    const int nv = V / vec_elems(dtype);
+    L.tiles = nv > kTileVecs ? (nv + kTileVecs - 1) / kTileVecs : 1;
+    const int64_t rows = static_cast<int64_t>(B) * W;
+    // Tiles of a warp: enough warps to fill the GPU come first, then longer
+    // segments (fewer partial sums and less start-up per byte).
+    const int64_t all = rows * L.tiles;
+    L.seg_tiles = W * L.tiles <= kSmallTiles || all < 1024 ? 1 : all < 4096 ? 2 : 4;
+    L.segs = (L.tiles + L.seg_tiles - 1) / L.seg_tiles;
     L.stats = kPartialBase;
-    L.keys = align_up(L.stats + chunks * sizeof(BeamStat), 256);
-    L.total = align_up(L.keys + chunks * static_cast<size_t>(K) * sizeof(uint64_t), 256);
+    L.peaks = align_up(L.stats + static_cast<size_t>(rows) * static_cast<size_t>(L.segs) * sizeof(BeamStat), 256);
+    L.total = align_up(L.peaks + static_cast<size_t>(rows) * static_cast<size_t>(L.tiles) * sizeof(float), 256);
     return L;
 }
 
 template <class Tag>
 specdec_status launch_beam(const BeamParams& P, cudaStream_t stream) {
-    const int64_t rows = static_cast<int64_t>(P.B) * P.W;
-    if (P.cpr > 65535) return SPECDEC_ERR_UNSUPPORTED;  // grid limit
-    const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(P.cpr));
-    if (launch_pdl(beam_pass_kernel<Tag, Tag::VEC>, grid, 0, stream, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
-    const int warps = P.W <= 8 ? 8 : P.W <= 16 ? 16 : 32;  // a warp per beam
-    if (launch_pdl(beam_merge_kernel, dim3(static_cast<unsigned>(P.B)), 0, stream, P, 32 * warps) != cudaSuccess)
+    if (P.W * P.tiles <= kSmallTiles) {
+        if (launch_pdl(beam_small_kernel<Tag, Tag::VEC>, dim3(static_cast<unsigned>(P.B)), 0, stream, P) != cudaSuccess)
+            return SPECDEC_ERR_CUDA;
+        return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+    }
+    const int64_t units = static_cast<int64_t>(P.B) * P.W * P.segs;
+    if (units > 0x7fffffff) return SPECDEC_ERR_UNSUPPORTED;  // units are counted in 32 bits
+    const unsigned ctas = static_cast<unsigned>((units + NWARPS - 1) / NWARPS);
+    if (launch_pdl(beam_pass_kernel<Tag, Tag::VEC>, dim3(ctas), 0, stream, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
+    if (launch_pdl(beam_merge_kernel<Tag, Tag::VEC>, dim3(static_cast<unsigned>(P.B)), 0, stream, P) != cudaSuccess)
         return SPECDEC_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+// One cluster over the batch: a CTA per kPlanThreads requests, up to kPlanCtas.
+cudaError_t launch_plan_tables(const PlanParams& P, cudaStream_t stream) {
+    const int need = (P.B + kPlanThreads - 1) / kPlanThreads;
+    const unsigned ctas = static_cast<unsigned>(need < kPlanCtas ? need : kPlanCtas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, plan_tables_kernel<false>, P);
 }
 
 // CTAs of a copy kernel: enough to fill the GPU several times over, each
@@ -1003,7 +1018,7 @@ size_t specdec_workspace_size_beam(int B, int W, int K, int V, specdec_dtype dty
     if (!dtype_ok(dtype) || B < 0 || B > SPECDEC_MAX_B || W < 1 || W > SPECDEC_MAX_BEAMS || K < 1 ||
         K > SPECDEC_MAX_BEAMS || V < 1 || V > SPECDEC_MAX_V)
         return 0;
-    return make_beam_layout(B, W, K, V, dtype).total;
+    return make_beam_layout(B, W, V, dtype).total;
 }
 
 specdec_status specdec_beam_select(const void* logits, specdec_dtype dtype, int64_t row_stride,
@@ -1023,7 +1038,7 @@ specdec_status specdec_beam_select(const void* logits, specdec_dtype dtype, int6
         return SPECDEC_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(logits) % static_cast<uintptr_t>(elem_size(dtype)) != 0)
         return SPECDEC_ERR_INVALID_ARG;
-    const BeamLayout L = make_beam_layout(B, W, K, V, dtype);
+    const BeamLayout L = make_beam_layout(B, W, V, dtype);
     specdec_status st = check_ws(ws, ws_bytes, L.total);
     if (st != SPECDEC_OK) return st;
     BeamParams P;
@@ -1036,9 +1051,11 @@ specdec_status specdec_beam_select(const void* logits, specdec_dtype dtype, int6
     P.K = K;
     P.V = V;
     P.eos = eos_token;
-    P.cpr = L.cpr;
+    P.tiles = L.tiles;
+    P.seg_tiles = L.seg_tiles;
+    P.segs = L.segs;
     P.stats = reinterpret_cast<BeamStat*>(static_cast<char*>(ws) + L.stats);
-    P.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + L.keys);
+    P.peaks = reinterpret_cast<float*>(static_cast<char*>(ws) + L.peaks);
     P.out_scores = out_scores;
     P.out_parents = out_parents;
     P.out_tokens = out_tokens;
@@ -1195,7 +1212,12 @@ specdec_status specdec_plan_slots(const int32_t* seq_lens, const int32_t* accept
     P.positions = positions;
     P.slots = slots;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (launch_pdl(plan_tables_kernel, dim3(1), 0, s, P, kPlanThreads) != cudaSuccess) return SPECDEC_ERR_CUDA;
+    const int64_t rows = draft_offsets != nullptr ? B + total_drafts : static_cast<int64_t>(B) * (k + 1);
+    if (B <= kPlanThreads && rows <= kPlanFusedRows) {
+        if (launch_pdl(plan_tables_kernel<true>, dim3(1), 0, s, P, kPlanThreads) != cudaSuccess) return SPECDEC_ERR_CUDA;
+        return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+    }
+    if (launch_plan_tables(P, s) != cudaSuccess) return SPECDEC_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>((B + NWARPS - 1) / NWARPS),
                     static_cast<unsigned>(static_cast<int64_t>(k) / kSlotTile + 1));
     if (launch_pdl(plan_slots_kernel, grid, 0, s, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
