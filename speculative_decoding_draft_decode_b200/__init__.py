@@ -21,9 +21,7 @@ There is no CPU fallback: if the CUDA library is missing, loading it raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
-import struct
 from typing import Optional
 
 __all__ = [
@@ -334,7 +332,6 @@ def ngram_propose(tokens, lengths, n_min: int = 2, n_max: int = 5, k: int = 4, p
     return (d[:, :k], n, off, packed) if pack else (d[:, :k], n)
 
 
-@functools.lru_cache(maxsize=1024)
 def specdec_workspace_size_beam(B: int, W: int, K: int, V: int, dtype: int) -> int:
     return lib().specdec_workspace_size_beam(B, W, K, V, dtype)
 
@@ -374,57 +371,34 @@ def specdec_plan_slots(seq_lens, accept_len, release, draft_offsets, B, k, total
 
 
 # ---------------------------------------------------------------------------
-# The caches around a verify step (torch layer).  These calls enqueue kernels
-# of a few microseconds, so their checks are kept to a few attribute reads.
+# The calls around a verify step (torch layer).  Their kernels take a few
+# microseconds, so the tensors are checked in native code (csrc/binding.cpp).
 # ---------------------------------------------------------------------------
-def _current(t):
-    """The current device, for a call whose arrays are on a GPU."""
-    if not t.is_cuda:
-        _on_current_device(t)
-    import torch
-    return torch.cuda.current_device()
+_native = None
 
 
-def _raw_stream(stream, cur):
-    """The stream handle of a call on the current device `cur`."""
-    if stream is None:
+def _bind():
+    global _native
+    if _native is None:
+        lib()  # raises if the library has not been built
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("_binding.so is not built (python -m speculative_decoding_draft_decode_b200.build): %s" % e)
+        _binding.load(library_path)
+        _native = _binding
+    return _native
+
+
+def _current(t, stream):
+    """The current device, for a call whose arrays are on a GPU, and the
+    stream handle (None: its current stream)."""
+    if stream is None and getattr(t, "is_cuda", False):
         import torch
-        return torch._C._cuda_getCurrentRawStream(cur)
-    return _stream(stream)
-
-
-def _want(t, dtype, shape, cur, name):
-    """Address of t, checked to be a contiguous tensor of that type and shape
-    on the current device `cur`."""
-    if t.get_device() != cur:
-        _on_current_device(t)
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, list(shape)))
-    return t.data_ptr()
-
-
-def _span(t):
-    """First and last byte + 1 of the memory a tensor's elements lie in."""
-    at = t.data_ptr()
-    if t.is_contiguous():
-        return at, at + t.numel() * t.element_size()
-    n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
-    return at, at + n * t.element_size()
-
-
-def _overlap(a, b):
-    (a0, a1), (b0, b1) = _span(a), _span(b)
-    return a0 < b1 and b0 < a1
-
-
-def _row_elems(shape, strides, lead, name):
-    """Elements of a row: the dimensions from `lead` on, which must lie one behind the other."""
-    n = 1
-    for d in range(len(shape) - 1, lead - 1, -1):
-        if strides[d] != n and shape[d] != 1:
-            raise ValueError("%s: the dimensions of a row must be contiguous" % name)
-        n *= shape[d]
-    return n
+        return torch.cuda.current_device(), None
+    _on_current_device(t, stream=stream)
+    import torch
+    return torch.cuda.current_device(), None if stream is None else _stream(stream)
 
 
 def _used_on(stream, *tensors):
@@ -435,9 +409,6 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
-_five = struct.Struct("5q").pack
-
-
 def reorder_states(states, parents, lengths=None, time_dim: int = 3, stream=None, out=None):
     """Row (b, i) of every group becomes row (b, parents[b, i]) over the
     positions below lengths[b] (all of them without lengths), after a beam
@@ -446,62 +417,11 @@ def reorder_states(states, parents, lengths=None, time_dim: int = 3, stream=None
     position a contiguous row.  parents int32 [B, W]; a row whose parent is
     outside [0, W) is left as it is.  In place, or into `out` (same shape and
     type, no overlap).  Returns what was written."""
-    import torch
-    shape = states.shape
-    if (time_dim != 3 and time_dim != 4) or len(shape) <= time_dim:
-        raise ValueError("states must be [G, B, W, T, ...] (time_dim 3) or [G, B, W, H, T, ...] (time_dim 4)")
-    cur = _current(states)
-    if states.get_device() != cur or stream is not None:
-        _on_current_device(states, stream=stream)
-    G, B, W = shape[:3]
-    p = _want(parents, torch.int32, (B, W), cur, "parents")
-    n = None if lengths is None else _want(lengths, torch.int32, (B,), cur, "lengths")
-    es = states.element_size()
-    strides = states.stride()
-    row = _row_elems(shape, strides, time_dim + 1, "states") * es
-    at = src = states.data_ptr()
-    to, dst = states, strides
-    if out is not None and out is not states:
-        to, dst, at = out, out.stride(), out.data_ptr()
-        if out.get_device() != cur:
-            _on_current_device(out)
-        if out.shape != shape or out.dtype is not states.dtype:
-            raise ValueError("out must have the shape and type of states")
-        _row_elems(shape, dst, time_dim + 1, "out")
-    if to.numel() == 0:
-        return to
-    if to is not states and not (at == src and dst == strides) and _overlap(states, to):
-        raise ValueError("out overlaps states: pass none to reorder in place")
-    if time_dim == 3:
-        g, b, w, t = dst[:4]
-        h, H, T, sh = 0, 1, shape[3], 0
-        sg, sb, sw, st = strides[:4]
-    else:
-        g, b, w, h, t = dst[:5]
-        H, T = shape[3:5]
-        sg, sb, sw, sh, st = strides[:5]
-    least = row // es
-    if (g < least and G > 1) or (b < least and B > 1) or (w < least and W > 1) or (h < least and H > 1) \
-            or (t < least and T > 1):
-        raise ValueError("the rows written must not share memory")
-    _check(lib().specdec_reorder_states(src, at, p, n, G, B, W, H, T, row,
-                                        _five(sg * es, sb * es, sw * es, sh * es, st * es),
-                                        _five(g * es, b * es, w * es, h * es, t * es), _raw_stream(stream, cur)),
-           "reorder_states")
-    return to
-
-
-def _slot_table(t, B, cur, name):
-    """Address, columns and row stride of an int64 [B, n] table of slots."""
-    import torch
-    if t.get_device() != cur:
-        _on_current_device(t)
-    if t.dtype is torch.int64 and t.dim() == 2:
-        rows, n = t.shape
-        rs, es = t.stride()
-        if rows == B and (es == 1 or n == 1) and (rs >= n or B == 1):
-            return t.data_ptr(), n, rs if rs > n else n
-    raise ValueError("%s must be an int64 [B, n] tensor with contiguous rows" % name)
+    cur, s = _current(states, stream)
+    st = _bind().reorder_states(states, parents, lengths, time_dim, out, s, cur)
+    if st:
+        raise SpecdecError(st, "reorder_states")
+    return states if out is None else out
 
 
 def commit_path(src, accept_len, accept_nodes, dst, dst_slots, src_slots=None, stream=None):
@@ -512,55 +432,10 @@ def commit_path(src, accept_len, accept_nodes, dst, dst_slots, src_slots=None, s
     ...]; dst [G, slots, ...]; dst_slots int64 [B, >= max_depth + 1] (for the
     slots of plan_slots with k = N: slots.view(B, N + 1)).  src and dst may be
     one cache when src_slots and dst_slots hold the same slots.  Returns dst."""
-    import torch
-    cur = _current(src)
-    if src.get_device() != cur or dst.get_device() != cur or stream is not None:
-        _on_current_device(src, dst, stream=stream)
-    if accept_nodes.dim() != 2:
-        raise ValueError("accept_nodes must be [B, max_depth]")
-    B, depth = shape = accept_nodes.shape
-    nodes_at = _want(accept_nodes, torch.int32, shape, cur, "accept_nodes")
-    len_at = _want(accept_len, torch.int32, (B,), cur, "accept_len")
-    lead = 3 if src_slots is None else 2
-    ss, ds = src.shape, dst.shape
-    if len(ss) < lead or len(ds) < 2 or src.dtype is not dst.dtype or ss[lead:] != ds[2:] or ss[0] != ds[0]:
-        raise ValueError("src must be [G, B, N + 1, ...] (with src_slots [G, S, ...]) and dst [G, slots, ...] of its type")
-    to_at, n, to_stride = _slot_table(dst_slots, B, cur, "dst_slots")
-    if n < depth + 1:
-        raise ValueError("dst_slots must have max_depth + 1 columns at least")
-    es = src.element_size()
-    s_src, s_dst = src.stride(), dst.stride()
-    row = _row_elems(ss, s_src, lead, "src")
-    _row_elems(ds, s_dst, 2, "dst")
-    src_at, dst_at = src.data_ptr(), dst.data_ptr()
-    if src_slots is None:
-        if ss[1] != B:
-            raise ValueError("src must be [G, B, N + 1, ...]")
-        from_at, src_rows, from_stride = None, 0, 0
-        nodes = ss[2]
-        sg, sb, sr = s_src[:3]
-        if nodes == 1 and sr < row:
-            sr = row
-        same = False
-    else:
-        from_at, nodes, from_stride = _slot_table(src_slots, B, cur, "src_slots")
-        src_rows, sb = ss[1], 0
-        sg, sr = s_src[:2]
-        if src_rows == 1 and sr < row:
-            sr = row
-        same = src_at == dst_at and s_src == s_dst
-    if src.numel() == 0 or dst.numel() == 0 or B == 0:
-        return dst
-    dg, dr = s_dst[:2]
-    if ds[1] == 1 and dr < row:
-        dr = row
-    if not same and _overlap(src, dst):
-        raise ValueError("src and dst overlap: in place both must be the same cache, with src_slots")
-    if dg < row and ds[0] > 1:
-        raise ValueError("the rows written must not share memory")
-    _check(lib().specdec_commit_path(src_at, sg * es, sb * es, sr * es, from_at, from_stride, src_rows, dst_at, dg * es,
-                                     dr * es, to_at, to_stride, ds[1], len_at, nodes_at, ss[0], B, nodes - 1, depth,
-                                     row * es, _raw_stream(stream, cur)), "commit_path")
+    cur, s = _current(src, stream)
+    st = _bind().commit_path(src, accept_len, accept_nodes, dst, dst_slots, src_slots, s, cur)
+    if st:
+        raise SpecdecError(st, "commit_path")
     return dst
 
 
@@ -573,47 +448,21 @@ def plan_slots(seq_lens, block_tables, held_blocks, free_ring, ring_state, block
     place; ring_state int32 [2] (head, count).  Returns (seq_lens, held_blocks,
     ring_state, positions int64 [rows], slots int64 [rows]): the new values,
     in `out` when given (whose first three may be the arrays they replace)."""
-    import torch
-    i32, i64 = torch.int32, torch.int64
-    cur = _current(seq_lens)
-    if stream is not None:
-        _on_current_device(stream=stream)
-    B = seq_lens.numel()
-    one = (B,)
-    if draft_offsets is not None:
-        offsets_at = _want(draft_offsets, i32, (B + 1,), cur, "draft_offsets")
-        rows = B + total_drafts
-    else:
-        offsets_at, rows = None, B * (k + 1)
-    if rows < 0:
-        raise ValueError("k and total_drafts must not be negative")
-    ring = free_ring.numel()
-    if block_tables.get_device() != cur:
-        _on_current_device(block_tables)
-    if block_tables.dtype is not i32 or block_tables.dim() != 2:
-        raise ValueError("block_tables must be an int32 [B, max_blocks] tensor with contiguous rows")
-    nb, cols = block_tables.shape
-    ts, es = block_tables.stride()
-    if nb != B or (es != 1 and cols != 1) or (ts < cols and B > 1):
-        raise ValueError("block_tables must be an int32 [B, max_blocks] tensor with contiguous rows")
+    cur, s = _current(seq_lens, stream)
     if out is None:
-        dev = seq_lens.device
-        out = (torch.empty(B, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
-               ring_state.clone() if B == 0 else torch.empty(2, dtype=i32, device=dev),
-               torch.empty(rows, dtype=i64, device=dev), torch.empty(rows, dtype=i64, device=dev))
+        import torch
+        B, i32 = seq_lens.numel(), dict(dtype=torch.int32, device=seq_lens.device)
+        rows = max(B * (k + 1) if draft_offsets is None else B + total_drafts, 0)
+        out = (torch.empty(B, **i32), torch.empty(B, **i32),
+               ring_state.clone() if B == 0 else torch.empty(2, **i32),
+               torch.empty(rows, dtype=torch.int64, device=seq_lens.device),
+               torch.empty(rows, dtype=torch.int64, device=seq_lens.device))
         _used_on(stream, *out)
-    lens, held, state, positions, slots = out
-    _check(lib().specdec_plan_slots(
-        _want(seq_lens, i32, one, cur, "seq_lens"),
-        None if accept_len is None else _want(accept_len, i32, one, cur, "accept_len"),
-        None if release is None else _want(release, i32, one, cur, "release"),
-        offsets_at, B, k, total_drafts, block_size, block_tables.data_ptr(), ts if ts > cols else cols, cols,
-        _want(held_blocks, i32, one, cur, "held_blocks"), _want(free_ring, i32, (ring,), cur, "free_ring"), ring,
-        _want(ring_state, i32, (2,), cur, "ring_state"), _want(lens, i32, one, cur, "out: seq_lens"),
-        _want(held, i32, one, cur, "out: held_blocks"), _want(state, i32, (2,), cur, "out: ring_state"),
-        _want(positions, i64, (rows,), cur, "out: positions"), _want(slots, i64, (rows,), cur, "out: slots"),
-        _raw_stream(stream, cur)), "plan_slots")
-    return lens, held, state, positions, slots
+    st = _bind().plan_slots(seq_lens, block_tables, held_blocks, free_ring, ring_state, block_size, k, draft_offsets,
+                            total_drafts, accept_len, release, out, s, cur)
+    if st:
+        raise SpecdecError(st, "plan_slots")
+    return out
 
 
 def specdec_set_prefetch_inputs(enable: bool) -> bool:
@@ -745,33 +594,24 @@ class Verifier:
         probabilities, -inf: no hypothesis), finished int32 [B, W] or None ->
         (scores float32 [B, num_beams], parents, tokens int32 [B, num_beams]),
         the best continuations in descending order."""
-        import torch
-        cur = _current(logits)
-        f32, i32 = torch.float32, torch.int32
-        if logits.get_device() != cur or stream is not None:
-            _on_current_device(logits, stream=stream)
+        cur, handle = _current(logits, stream)
         if self.device.index != cur:
             self._on_device(logits)
-        dt = _dtype_code(logits)
-        stride = _row_stride(logits, "logits")
-        B, W, V = logits.shape
-        K = num_beams
-        shape = (B, K if K > 0 else 0)
         if out is None:
-            dev = logits.device
-            out = (torch.empty(shape, dtype=f32, device=dev), torch.empty(shape, dtype=i32, device=dev),
-                   torch.empty(shape, dtype=i32, device=dev))
+            import torch
+            shape, dev = (logits.shape[0], max(num_beams, 0)), logits.device
+            out = (torch.empty(shape, dtype=torch.float32, device=dev), torch.empty(shape, dtype=torch.int32, device=dev),
+                   torch.empty(shape, dtype=torch.int32, device=dev))
             _used_on(stream, *out)
-        scores, parents, tokens = out
-        L = lib()
-        ws, wsb = self.workspace(specdec_workspace_size_beam(B, W, K, V, dt), stream)
-        _check(L.specdec_beam_select(
-            logits.data_ptr(), dt, stride, _want(beam_scores, f32, (B, W), cur, "beam_scores"),
-            None if finished is None else _want(finished, i32, (B, W), cur, "finished"), eos_token, B, W, K, V,
-            _want(scores, f32, shape, cur, "out: scores"), _want(parents, i32, shape, cur, "out: parents"),
-            _want(tokens, i32, shape, cur, "out: tokens"), None if ws is None else ws.data_ptr(), wsb,
-            _raw_stream(stream, cur)), "beam_select")
-        return scores, parents, tokens
+        select = _bind().beam_select
+        st = select(logits, beam_scores, num_beams, finished, eos_token, out, self._ws, self._ws_bytes, handle, cur)
+        if st == SPECDEC_ERR_WORKSPACE:  # the first call, or a larger one than any before
+            B, W, V = logits.shape
+            need = specdec_workspace_size_beam(B, W, num_beams, V, _dtype_code(logits))
+            ws, wsb = self.workspace(need, stream)
+            st = select(logits, beam_scores, num_beams, finished, eos_token, out, ws, wsb, handle, cur)
+        _check(st, "beam_select")
+        return out
 
     def tree(self, logits, parents, node_tokens, max_depth: int, stream=None, out=None):
         """logits [B, N+1, V], parents/node_tokens [B, N+1] int32 ->

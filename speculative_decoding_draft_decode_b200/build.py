@@ -1,10 +1,16 @@
-"""Build the verifier's CUDA library (libspecdec.so) in the package folder.
+"""Build the package's native code, in the package folder.
+
+The verifier's CUDA library:
 
     nvcc -O3 -std=c++17 -gencode arch=compute_100a,code=sm_100a -lineinfo
          -Xcompiler -fPIC -shared csrc/specdec_api.cu -o libspecdec.so
 
 The CUDA runtime is linked statically, so the library loads next to any
 PyTorch build.  No fast-math: the rejection statistics rely on IEEE expf.
+
+The torch binding of the calls around the verify step (_binding.so, from
+csrc/binding.cpp): host code only, against the headers of the PyTorch that is
+installed.
 """
 from __future__ import annotations
 
@@ -12,16 +18,20 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libspecdec.so")
+BINDING = os.path.join(HERE, "_binding.so")
 MAIN = os.path.join(HERE, "csrc", "specdec_api.cu")
+BINDING_MAIN = os.path.join(HERE, "csrc", "binding.cpp")
+HEADER = os.path.join(ROOT, "include", "specdec.h")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(HERE, "csrc", "*"))) + [os.path.join(ROOT, "include", "specdec.h")]
+    return [s for s in sorted(glob.glob(os.path.join(HERE, "csrc", "*"))) if s != BINDING_MAIN] + [HEADER]
 
 
 def nvcc():
@@ -31,16 +41,18 @@ def nvcc():
     return "nvcc"
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, srcs) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(s) <= t for s in srcs)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+def up_to_date() -> bool:
+    return _newer(LIB, sources()) and _newer(BINDING, [BINDING_MAIN, HEADER])
+
+
+def _build_library(verbose: bool) -> None:
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
            "-cudart", "static", MAIN, "-o", tmp]
@@ -49,6 +61,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+
+
+def _build_binding(verbose: bool) -> None:
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+           BINDING_MAIN, "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-ldl"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if force or not _newer(LIB, sources()):
+        _build_library(verbose)
+    if force or not _newer(BINDING, [BINDING_MAIN, HEADER]):
+        _build_binding(verbose)
     return LIB
 
 

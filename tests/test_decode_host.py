@@ -37,7 +37,7 @@ def test_beam_refusals():
 def test_beam_workspace_size():
     f = sd.specdec_workspace_size_beam
     assert f(64, 8, 8, 128256, sd.SPECDEC_BF16) > 65536 * 4
-    assert f(64, 8, 16, 128256, sd.SPECDEC_BF16) > f(64, 8, 8, 128256, sd.SPECDEC_BF16)
+    assert f(64, 16, 8, 128256, sd.SPECDEC_BF16) > f(64, 8, 8, 128256, sd.SPECDEC_BF16)
     assert f(0, 8, 8, 1000, 0) >= 65536 * 4
     for bad in ((-1, 4, 4, 100, 0), (4, 0, 4, 100, 0), (4, 33, 4, 100, 0), (4, 4, 0, 100, 0), (4, 4, 33, 100, 0),
                 (4, 4, 4, 0, 0), (4, 4, 4, 100, 2)):
@@ -120,30 +120,44 @@ class OnGpu1:
     """Stands for a tensor of another GPU."""
     device = torch.device("cuda", 1)
     is_cuda = True
-    dtype = torch.float32
-    shape = (1, 2, 3, 4, 5)
-
-    def dim(self):
-        return 5
-
-    def get_device(self):
-        return 1
 
     def numel(self):
         return 2
 
 
-def test_other_devices_are_refused(monkeypatch):
+def test_other_streams_are_refused(monkeypatch):
+    """A stream of another device than the current one is refused before the
+    native code sees anything."""
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     x = OnGpu1()
-    with pytest.raises(ValueError, match="current device"):
-        sd.Verifier(torch.device("cuda", 0)).beam_select(x, x, 3)
-    with pytest.raises(ValueError, match="current device"):
-        sd.reorder_states(x, x)
-    with pytest.raises(ValueError, match="current device"):
-        sd.commit_path(x, x, x, x, x)
-    with pytest.raises(ValueError, match="current device"):
-        sd.plan_slots(x, x, x, x, x, 16)
+
+    class Here(OnGpu1):
+        device = torch.device("cuda", 0)
+
+    for args in (dict(stream=x), dict(stream=OnGpu1())):
+        for t in (x, Here()):
+            with pytest.raises(ValueError, match="current device"):
+                sd.Verifier(torch.device("cuda", 0)).beam_select(t, t, 3, **args)
+            with pytest.raises(ValueError, match="current device"):
+                sd.reorder_states(t, t, **args)
+            with pytest.raises(ValueError, match="current device"):
+                sd.commit_path(t, t, t, t, t, **args)
+            with pytest.raises(ValueError, match="current device"):
+                sd.plan_slots(t, t, t, t, t, 16, **args)
+
+
+def test_binding_refuses_what_is_no_tensor():
+    b = sd._bind()
+    with pytest.raises(TypeError):
+        b.reorder_states([1], None, None, 3, None, None, 0)
+    with pytest.raises(TypeError):
+        b.reorder_states()
+    with pytest.raises(TypeError):
+        b.plan_slots(*[None] * 14)
+    with pytest.raises(OverflowError):
+        b.commit_path(*[torch.zeros(1)] * 6, None, 1 << 80)
+    with pytest.raises(ValueError, match="CUDA device tensors"):
+        b.reorder_states(torch.zeros(1, 1, 1, 1, 4), torch.zeros(1, 1).int(), None, 3, None, None, 0)
 
 
 def test_outgrown_workspaces_are_kept(monkeypatch):

@@ -223,3 +223,20 @@ def test_commit_refusals(torch_, sd_):
             ok(**bad)
     with pytest.raises(sd_.SpecdecError):
         sd_.commit_path(src, i(3), i(3, 33), dst, torch.zeros(3, 34, dtype=torch.int64, device="cuda"))
+
+
+def test_other_current_device_is_refused(torch_, sd_, monkeypatch):
+    """Tensors of another device than the current one: refused, nothing launched."""
+    torch = torch_
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    x, p = torch.zeros(1, 2, 3, 4, 5, device="cuda"), torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError, match="current device"):
+        sd_.reorder_states(x, p)
+    with pytest.raises(ValueError, match="current device"):
+        sd_.commit_path(torch.zeros(1, 2, 3, 4, device="cuda"), i(2), i(2, 2), torch.zeros(1, 9, 4, device="cuda"),
+                        torch.zeros(2, 3, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="current device"):
+        sd_.plan_slots(i(2), i(2, 4), i(2), i(10), i(2), 16, out=(i(2), i(2), i(2), i(2).long(), i(2).long()))
+    with pytest.raises(ValueError):
+        sd_.Verifier(torch.device("cuda", 0)).beam_select(x[0, 0].contiguous(), torch.zeros(3, 4, device="cuda"), 2)
