@@ -405,31 +405,31 @@ __device__ __noinline__ int beam_many_tiles(const BeamParams& P, const float* pe
     return P.K;
 }
 
-// Every element of the n best tiles with a value of at least `bound`, and the
-// finished beams: f(c, w V + token).  A warp per tile.
-template <class Tag, int VEC, class F>
-__device__ __forceinline__ void beam_visit(const BeamParams& P, int64_t b, int n, double bound, const BeamMergeSmem& sm, F f) {
+// One of the K best tiles, as a warp reads it again.
+template <class Tag, int VEC>
+struct BeamPlace {
     using Elem = typename Tag::storage;
-    const int wp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t V = static_cast<uint32_t>(P.V);
-    struct Place {
-        const Elem* row;
-        RowCut cut;
-        int w, tile, ie;
-        float xe;
-    };
-    auto load = [&](int i, BeamTile<Tag, VEC>& a) {
-        Place p;
-        p.w = static_cast<int>(sm.tile_id[i]) / P.tiles;
-        p.tile = static_cast<int>(sm.tile_id[i]) - p.w * P.tiles;
-        p.row = static_cast<const Elem*>(P.logits) + (b * P.W + p.w) * P.row_stride;
-        p.cut = cut_row<Tag, VEC>(p.row, P.V);
-        a.load(p.row, p.cut, p.tile);
-        p.xe = beam_end<Tag>(p.row, p.cut, P.V, p.tile == 0, p.tile == P.tiles - 1, p.ie);
-        return p;
-    };
-    auto look = [&](const Place& p, const BeamTile<Tag, VEC>& a) {
-        const int w = p.w;
+    BeamTile<Tag, VEC> a;
+    RowCut cut;
+    int w, tile, ie;  // ie: this lane's element of the row's head or tail, -1 if it has none
+    float xe;
+    __device__ __forceinline__ void load(const BeamParams& P, int64_t b, const BeamMergeSmem& sm, int i) {
+        w = static_cast<int>(sm.tile_id[i]) / P.tiles;
+        tile = static_cast<int>(sm.tile_id[i]) - w * P.tiles;
+        const Elem* row = static_cast<const Elem*>(P.logits) + (b * P.W + w) * P.row_stride;
+        cut = cut_row<Tag, VEC>(row, P.V);
+        a.load(row, cut, tile);
+        xe = beam_end<Tag>(row, cut, P.V, tile == 0, tile == P.tiles - 1, ie);
+    }
+    // The best value among this lane's elements.
+    __device__ __forceinline__ double best(const BeamMergeSmem& sm) const {
+        const float m = fmaxf(a.most(), xe);
+        return m > -INFINITY ? beam_value(sm, w, m) : -INFINITY;
+    }
+    // Every element of this lane with a value of at least `bound`: f(c, w V + token).
+    template <class F>
+    __device__ __forceinline__ void look(const BeamMergeSmem& sm, uint32_t V, double bound, F f) const {
+        const int lane = threadIdx.x & 31;
         // A logit below this has a value below the bound (the margin covers the
         // rounding of the fp64 sums); what passes is compared in fp64.
         const double at = (bound - sm.s[w]) + sm.logS[w] + sm.M[w];
@@ -441,26 +441,70 @@ __device__ __forceinline__ void beam_visit(const BeamParams& P, int64_t b, int n
                 if (c >= bound) f(c, static_cast<uint32_t>(w) * V + static_cast<uint32_t>(e));
             }
         };
-        if (p.ie >= 0) offer(p.xe, p.ie);
+        if (ie >= 0) offer(xe, ie);
 #pragma unroll
         for (int u = 0; u < kTileU; ++u) {
             if (!(VecOps<Tag, VEC>::vmax(a.w[u]) >= low)) continue;
-            const int e0 = p.cut.head + (p.tile * kTileVecs + u * 32 + lane) * VEC;
+            const int e0 = cut.head + (tile * kTileVecs + u * 32 + lane) * VEC;
 #pragma unroll
             for (int q = 0; q < VEC; ++q) offer(VecOps<Tag, VEC>::elem(a.w[u], q), e0 + q);
         }
-    };
-    for (int i = wp; i < n; i += 2 * NWARPS) {  // two tiles on their way
-        BeamTile<Tag, VEC> x, y;
-        const Place p = load(i, x);
-        Place q = p;
-        if (i + NWARPS < n) q = load(i + NWARPS, y);
-        look(p, x);
-        if (i + NWARPS < n) look(q, y);
     }
-    for (int w = threadIdx.x; w < P.W; w += NT)
-        if (sm.state[w] == 2 && sm.s[w] >= bound)
-            f(sm.s[w], static_cast<uint32_t>(w) * V + static_cast<uint32_t>(P.eos));
+};
+
+// A bound that K candidates reach, from the best one of each thread (rounded
+// down to fp32): the K-th largest of the 32 values that the warps' 4 best lanes
+// make up; -inf if there are fewer.  CTA-collective.
+__device__ __forceinline__ double beam_bound(double best, int K, BeamMergeSmem& sm) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    constexpr int kEach = 32 / NWARPS;
+    int o = ord_i32(__double2float_rd(best)), mine = INT_MIN;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int x = __reduce_max_sync(FULL_MASK, o);
+        if (lane == i) mine = x;
+        const unsigned who = __ballot_sync(FULL_MASK, o == x);
+        if (lane == __ffs(who) - 1) o = INT_MIN;
+    }
+    if (lane < kEach) sm.pool[wp * kEach + lane] = mine;
+    __syncthreads();
+    const int kth = warp_kth(sm.pool[lane], K);
+    __syncthreads();  // the pool may be written again
+    return kth == INT_MIN ? -INFINITY : static_cast<double>(from_ord_i32(kth));
+}
+
+// This thread's finished beam, if it has one (W <= kMaxBeams <= NT).
+__device__ __forceinline__ bool beam_ended(const BeamParams& P, const BeamMergeSmem& sm) {
+    return static_cast<int>(threadIdx.x) < P.W && sm.state[threadIdx.x] == 2;
+}
+template <class F>
+__device__ __forceinline__ void beam_look_ended(const BeamParams& P, const BeamMergeSmem& sm, double bound, F f) {
+    if (beam_ended(P, sm) && sm.s[threadIdx.x] >= bound)
+        f(sm.s[threadIdx.x], threadIdx.x * static_cast<uint32_t>(P.V) + static_cast<uint32_t>(P.eos));
+}
+
+// Every candidate of the n best tiles and the finished beams with a value of at
+// least `bound`.  A warp per tile.
+template <class Tag, int VEC, class F>
+__device__ __forceinline__ void beam_visit(const BeamParams& P, int64_t b, int n, double bound, const BeamMergeSmem& sm, F f) {
+    BeamPlace<Tag, VEC> x;
+    for (int i = threadIdx.x >> 5; i < n; i += NWARPS) {
+        x.load(P, b, sm, i);
+        x.look(sm, static_cast<uint32_t>(P.V), bound, f);
+    }
+    beam_look_ended(P, sm, bound, f);
+}
+
+// The bound of the best candidate of every thread over the n tiles.
+template <class Tag, int VEC>
+__device__ __noinline__ double beam_visit_bound(const BeamParams& P, int64_t b, int n, BeamMergeSmem& sm) {
+    double best = beam_ended(P, sm) ? sm.s[threadIdx.x] : -INFINITY;
+    BeamPlace<Tag, VEC> x;
+    for (int i = threadIdx.x >> 5; i < n; i += NWARPS) {
+        x.load(P, b, sm, i);
+        best = fmax(best, x.best(sm));
+    }
+    return beam_bound(best, P.K, sm);
 }
 
 // The outputs of more than kMergeCand candidates: the best one behind the last
@@ -554,17 +598,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         const int i = nth(j);
         if (i < total) best = fmax(best, value(i, __ldcg(&peaks[i])));
     }
-    int o = ord_i32(__double2float_rd(best)), mine = INT_MIN;
-    for (int i = 0; i < 32 / NWARPS; ++i) {
-        const int x = __reduce_max_sync(FULL_MASK, o);
-        if (lane == i) mine = x;
-        const unsigned who = __ballot_sync(FULL_MASK, o == x);
-        if (lane == __ffs(who) - 1) o = INT_MIN;
-    }
-    if (lane < 32 / NWARPS) sm.pool[wp * (32 / NWARPS) + lane] = mine;
-    __syncthreads();
-    const int kth = warp_kth(sm.pool[lane], K);
-    const double floor = kth == INT_MIN ? -INFINITY : static_cast<double>(from_ord_i32(kth));
+    const double floor = beam_bound(best, K, sm);
     auto keep = [&](double v, int i) {
         if (!(v >= floor && v > -INFINITY)) return;
         const int at = atomicAdd(&sm.tiles, 1);
@@ -598,26 +632,84 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         n = beam_many_tiles(P, peaks, sm);
     }
     __syncthreads();
-    const double bound = n == K ? sm.tile_c[K - 1] : -INFINITY;
-    beam_visit<Tag, VEC>(P, b, n, bound, sm, [&](double v, uint32_t id) {
+    double bound = n == K ? sm.tile_c[K - 1] : -INFINITY;
+    auto take = [&](double v, uint32_t id) {
         const int at = atomicAdd(&sm.cands, 1);
         if (at < kMergeCand) {
             sm.c[at] = v;
             sm.id[at] = id;
         }
-    });
+    };
+    // Few tiles to choose from bound the elements badly: the threads' best
+    // elements do better.
+    const bool few = total < 8 * K;
+    if (n <= 2 * NWARPS) {  // two tiles a warp, held in registers
+        BeamPlace<Tag, VEC> x, y;
+        const bool has_x = wp < n, has_y = wp + NWARPS < n;
+        if (has_x) x.load(P, b, sm, wp);
+        if (has_y) y.load(P, b, sm, wp + NWARPS);
+        if (few) {
+            double e = beam_ended(P, sm) ? sm.s[t] : -INFINITY;
+            if (has_x) e = fmax(e, x.best(sm));
+            if (has_y) e = fmax(e, y.best(sm));
+            bound = fmax(bound, beam_bound(e, K, sm));
+        }
+        if (has_x) x.look(sm, static_cast<uint32_t>(P.V), bound, take);
+        if (has_y) y.look(sm, static_cast<uint32_t>(P.V), bound, take);
+        beam_look_ended(P, sm, bound, take);
+    } else {
+        if (few) bound = fmax(bound, beam_visit_bound<Tag, VEC>(P, b, n, sm));
+        beam_visit<Tag, VEC>(P, b, n, bound, sm, take);
+    }
     __syncthreads();
-    const int cands = sm.cands;
+    int cands = sm.cands;
+    if (cands > kMergeCand && !few) {  // the tiles' many elements above the K-th tile's best
+        bound = fmax(bound, beam_visit_bound<Tag, VEC>(P, b, n, sm));
+        if (t == 0) sm.cands = 0;
+        __syncthreads();
+        beam_visit<Tag, VEC>(P, b, n, bound, sm, take);
+        __syncthreads();
+        cands = sm.cands;
+    }
     if (cands > kMergeCand) {
         beam_many_candidates<Tag, VEC>(P, b, n, bound, sm);
         return;
     }
-    for (int i = t; i < cands; i += NT) {
-        const double v = sm.c[i];
-        const uint32_t id = sm.id[i];
+    // A candidate's rank is its place.  Among many, those below the bound of
+    // the threads' best ones have none.
+    double own_c[kMergeCand / NT];
+    uint32_t own_id[kMergeCand / NT];
+    double e = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kMergeCand / NT; ++j) {
+        const int i = t + j * NT;
+        own_c[j] = i < cands ? sm.c[i] : -INFINITY;
+        own_id[j] = i < cands ? sm.id[i] : 0u;
+        e = fmax(e, own_c[j]);
+    }
+    int ranked = cands;
+    if (cands > 64) {
+        const double least = beam_bound(e, K, sm);  // its barriers: every candidate has been read
+        if (t == 0) sm.cands = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kMergeCand / NT; ++j) {
+            if (!(own_c[j] >= least)) own_c[j] = -INFINITY;
+            if (own_c[j] > -INFINITY) {
+                const int at = atomicAdd(&sm.cands, 1);
+                sm.c[at] = own_c[j];
+                sm.id[at] = own_id[j];
+            }
+        }
+        __syncthreads();
+        ranked = sm.cands;
+    }
+#pragma unroll
+    for (int j = 0; j < kMergeCand / NT; ++j) {
+        if (!(own_c[j] > -INFINITY)) continue;
         int rank = 0;
-        for (int j = 0; j < cands; ++j) rank += beam_before(sm.c[j], sm.id[j], v, id) ? 1 : 0;
-        if (rank < K) beam_output(P, b * K + rank, v, id);
+        for (int i = 0; i < ranked; ++i) rank += beam_before(sm.c[i], sm.id[i], own_c[j], own_id[j]) ? 1 : 0;
+        if (rank < K) beam_output(P, b * K + rank, own_c[j], own_id[j]);
     }
     for (int i = cands + t; i < K; i += NT) {
         P.out_scores[b * K + i] = -INFINITY;

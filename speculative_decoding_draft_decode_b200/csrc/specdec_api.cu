@@ -274,25 +274,39 @@ cudaError_t launch_plan_tables(const PlanParams& P, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, plan_tables_kernel<false>, P);
 }
 
-// CTAs of a copy kernel: enough to fill the GPU several times over, each
-// taking the next work item in turn.
-unsigned copy_grid(int64_t items) {
-    constexpr int64_t kMost = 148 * 16;
-    return static_cast<unsigned>(items < kMost ? items : kMost);
+constexpr int64_t kCopyCtas = 148 * 16;  // CTAs of a copy kernel: the GPU several times over
+
+// Runs of a beam's positions from which unaligned ones are put together from
+// aligned words.
+constexpr int64_t kShiftBytes = 256;
+
+// Grid of a copy kernel: requests and groups first, then as many column tiles
+// as it takes to fill the GPU.
+dim3 tile_grid(int64_t tiles, int B, int64_t groups) {
+    const unsigned z = static_cast<unsigned>(groups < 65535 ? groups : 65535);
+    const unsigned y = static_cast<unsigned>(B < 65535 ? B : 65535);
+    const int64_t room = kCopyCtas / (static_cast<int64_t>(y) * z) + 1;
+    return dim3(static_cast<unsigned>(tiles < room ? tiles : room), y, z);
 }
 
 template <class VT, int WT, int C>
-specdec_status launch_reorder_as(ReorderParams P, cudaStream_t stream) {
-    P.tiles = (P.T * P.row + NT * C - 1) / (NT * C);
-    const int64_t items = P.G * P.H * P.B * P.tiles;
-    if (launch_pdl(reorder_states_kernel<VT, WT, C>, dim3(copy_grid(items)), 0, stream, P) != cudaSuccess)
-        return SPECDEC_ERR_CUDA;
+specdec_status launch_reorder_as(const ReorderParams& P, cudaStream_t stream) {
+    const dim3 grid = tile_grid((P.T * P.row + NT * C - 1) / (NT * C), P.B, P.G * P.H);
+    if (launch_pdl(reorder_states_kernel<VT, WT, C>, grid, 0, stream, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+specdec_status launch_reorder_shift(ReorderParams P, int64_t row_bytes, cudaStream_t stream) {
+    P.row = row_bytes;
+    const dim3 grid = tile_grid((P.T * row_bytes + NT * 16 - 1) / (NT * 16), P.B, P.G * P.H);
+    if (launch_pdl(reorder_shift_kernel, grid, 0, stream, P) != cudaSuccess) return SPECDEC_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 template <class VT>
 specdec_status launch_reorder(ReorderParams P, int64_t row_bytes, cudaStream_t stream) {
     P.row = row_bytes / static_cast<int64_t>(sizeof(VT));
+    P.narrow = static_cast<double>(P.T) * static_cast<double>(P.row) < 4e9 ? 1 : 0;
     if (P.W <= 2) return launch_reorder_as<VT, 2, 8>(P, stream);
     if (P.W <= 4) return launch_reorder_as<VT, 4, 4>(P, stream);
     if (P.W <= 8) return launch_reorder_as<VT, 8, 2>(P, stream);
@@ -303,10 +317,8 @@ specdec_status launch_reorder(ReorderParams P, int64_t row_bytes, cudaStream_t s
 template <class VT>
 specdec_status launch_commit(CommitParams P, int64_t row_bytes, cudaStream_t stream) {
     P.row = row_bytes / static_cast<int64_t>(sizeof(VT));
-    P.tiles = (P.row + NT - 1) / NT;
-    const int64_t items = P.G * P.B * P.tiles;
-    if (launch_pdl(commit_path_kernel<VT>, dim3(copy_grid(items)), 0, stream, P) != cudaSuccess)
-        return SPECDEC_ERR_CUDA;
+    const dim3 grid = tile_grid((P.row + kCommitThreads - 1) / kCommitThreads, P.B, P.G);
+    if (launch_pdl(commit_path_kernel<VT>, grid, 0, stream, P, kCommitThreads) != cudaSuccess) return SPECDEC_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
@@ -1114,6 +1126,9 @@ specdec_status specdec_reorder_states(const void* src, void* dst, const int32_t*
     if (bits % 16 == 0) return launch_reorder<uint4>(P, row_bytes, s);
     if (bits % 8 == 0) return launch_reorder<uint2>(P, row_bytes, s);
     if (bits % 4 == 0) return launch_reorder<uint32_t>(P, row_bytes, s);
+    // 9 beams of 472 x 249 bf16 in 28 groups: 21.9 us put together from aligned
+    // words, 33.9 us in 2-byte accesses (4-byte accesses beat both).
+    if (!P.in_place && P.flat && T * row_bytes >= kShiftBytes) return launch_reorder_shift(P, row_bytes, s);
     if (bits % 2 == 0) return launch_reorder<uint16_t>(P, row_bytes, s);
     return launch_reorder<uint8_t>(P, row_bytes, s);
 }
