@@ -291,9 +291,10 @@ struct BeamMergeSmem {
     double M[kMaxBeams];     // near the row's largest logit
     double logS[kMaxBeams];  // log sum exp(l - M)
     double s[kMaxBeams];
+    double add[kMaxBeams];   // s - M - logS
     int state[kMaxBeams];    // 0: no candidates, 1: streamed, 2: finished
     double c[kMergeCand];    // tiles, then candidates
-    uint32_t id[kMergeCand];
+    uint32_t id[kMergeCand];    // their names
     double tile_c[kMaxBeams];   // the K best tiles
     uint32_t tile_id[kMaxBeams];
     int pool[32];
@@ -302,43 +303,65 @@ struct BeamMergeSmem {
     int tiles, cands;
 };
 
+// c of a logit of row w: one addition, or, where M is so large that s and logS
+// would be lost beside it, the difference of the large numbers first.
+constexpr double kBeamPlain = 1e6;
 __device__ __forceinline__ double beam_value(const BeamMergeSmem& sm, int w, float x) {
-    return (sm.s[w] + (static_cast<double>(x) - sm.M[w])) - sm.logS[w];
+    const double M = sm.M[w];
+    if (fabs(M) < kBeamPlain) return static_cast<double>(x) + sm.add[w];
+    return (sm.s[w] + (static_cast<double>(x) - M)) - sm.logS[w];
 }
 
-// Segment i of a row's n.
-__device__ __forceinline__ BeamStat beam_stat(const BeamStat* p, int i, int n) {
-    BeamStat x;
-    x.M = -DBL_MAX;
-    x.S = 0.0;
-    if (i < n) {
-        x.M = __ldcg(&p[i].M);
-        x.S = __ldcg(&p[i].S);
+// Candidates are named (w << 24) + token and tiles (w << 16) + tile: both in
+// the order of w V + token.
+constexpr int kTokenBits = 24, kTileBits = 16;
+
+// A lane's part of a row's n segments: kSegs of them, 32 apart, from i0 on.
+constexpr int kSegs = 4;
+struct BeamSegs {
+    double M[kSegs], S[kSegs];
+    __device__ __forceinline__ void load(const BeamStat* p, int i0, int n) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 0; j < kSegs; ++j) {
+            const int i = i0 + j * 32 + lane;
+            M[j] = -DBL_MAX;
+            S[j] = 0.0;
+            if (i < n) {
+                M[j] = __ldcg(&p[i].M);
+                S[j] = __ldcg(&p[i].S);
+            }
+        }
     }
-    return x;
-}
+};
 
-// A row's sum from its segments': 32 at a time (first: this lane's of the first
-// 32), each against the largest reference of the 32.  Warp-collective.
-__device__ __forceinline__ BeamStat beam_row_sum(const BeamStat* p, int n, BeamStat first) {
-    const int lane = threadIdx.x & 31;
+// A row's sum from its segments' (x: the first 32 kSegs), each against about
+// the largest reference of those loaded with it.  Warp-collective.
+__device__ __forceinline__ BeamStat beam_row_sum(const BeamStat* p, int n, BeamSegs x) {
     BeamStat acc;
     acc.M = -DBL_MAX;
     acc.S = 0.0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const BeamStat x = i0 == 0 ? first : beam_stat(p, i0 + lane, n);
-        const double M = x.M;
-        double S = x.S, top = S != 0.0 ? fmax(M, acc.M) : acc.M;
+    for (int i0 = 0;;) {
+        float m = -FLT_MAX;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(FULL_MASK, top, o));
-        if (S != 0.0 && M != top) S *= exp(M - top);
+        for (int j = 0; j < kSegs; ++j)
+            if (x.S[j] != 0.0) m = fmaxf(m, static_cast<float>(x.M[j]));
+        m = from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(m)));
+        double top = static_cast<double>(m);
+        if (acc.S != 0.0) top = fmax(top, acc.M);
+        double S = 0.0;
+#pragma unroll
+        for (int j = 0; j < kSegs; ++j)
+            if (x.S[j] != 0.0) S += x.S[j] * exp(x.M[j] - top);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(FULL_MASK, S, o);
-        if (acc.S != 0.0) S += acc.M != top ? acc.S * exp(acc.M - top) : acc.S;
+        if (acc.S != 0.0) S += acc.S * exp(acc.M - top);
         acc.M = top;
         acc.S = S;
+        i0 += 32 * kSegs;
+        if (i0 >= n) return acc;
+        x.load(p, i0, n);
     }
-    return acc;
 }
 
 // The best (c, id), larger c first and then the lower id, of one per thread.
@@ -375,10 +398,10 @@ __device__ __forceinline__ BeamBest beam_block_best(BeamBest x, BeamMergeSmem& s
     return x;
 }
 
-__device__ __forceinline__ void beam_output(const BeamParams& P, int64_t at, double c, uint32_t flat) {
+__device__ __forceinline__ void beam_output(const BeamParams& P, int64_t at, double c, uint32_t id) {
     P.out_scores[at] = static_cast<float>(c);
-    P.out_parents[at] = static_cast<int32_t>(flat / static_cast<uint32_t>(P.V));
-    P.out_tokens[at] = static_cast<int32_t>(flat % static_cast<uint32_t>(P.V));
+    P.out_parents[at] = static_cast<int32_t>(id >> kTokenBits);
+    P.out_tokens[at] = static_cast<int32_t>(id & ((1u << kTokenBits) - 1u));
 }
 
 // The K best tiles of more than kMergeTiles at the bound (runs of equal
@@ -393,7 +416,8 @@ __device__ __noinline__ int beam_many_tiles(const BeamParams& P, const float* pe
             const float m = sm.state[w] == 1 ? __ldcg(&peaks[j]) : -INFINITY;
             if (!(m > -INFINITY)) continue;
             const double c = beam_value(sm, w, m);
-            if (beam_before(last.c, last.id, c, j) && beam_before(c, j, best.c, best.id)) best = {c, static_cast<uint32_t>(j)};
+            const uint32_t id = (static_cast<uint32_t>(w) << kTileBits) + static_cast<uint32_t>(j - w * P.tiles);
+            if (beam_before(last.c, last.id, c, id) && beam_before(c, id, best.c, best.id)) best = {c, id};
         }
         last = beam_block_best(best, sm);
         if (last.id == 0xffffffffu) return i;
@@ -414,8 +438,8 @@ struct BeamPlace {
     int w, tile, ie;  // ie: this lane's element of the row's head or tail, -1 if it has none
     float xe;
     __device__ __forceinline__ void load(const BeamParams& P, int64_t b, const BeamMergeSmem& sm, int i) {
-        w = static_cast<int>(sm.tile_id[i]) / P.tiles;
-        tile = static_cast<int>(sm.tile_id[i]) - w * P.tiles;
+        w = static_cast<int>(sm.tile_id[i] >> kTileBits);
+        tile = static_cast<int>(sm.tile_id[i] & ((1u << kTileBits) - 1u));
         const Elem* row = static_cast<const Elem*>(P.logits) + (b * P.W + w) * P.row_stride;
         cut = cut_row<Tag, VEC>(row, P.V);
         a.load(row, cut, tile);
@@ -426,9 +450,9 @@ struct BeamPlace {
         const float m = fmaxf(a.most(), xe);
         return m > -INFINITY ? beam_value(sm, w, m) : -INFINITY;
     }
-    // Every element of this lane with a value of at least `bound`: f(c, w V + token).
+    // Every element of this lane with a value of at least `bound`: f(c, id).
     template <class F>
-    __device__ __forceinline__ void look(const BeamMergeSmem& sm, uint32_t V, double bound, F f) const {
+    __device__ __forceinline__ void look(const BeamMergeSmem& sm, double bound, F f) const {
         const int lane = threadIdx.x & 31;
         // A logit below this has a value below the bound (the margin covers the
         // rounding of the fp64 sums); what passes is compared in fp64.
@@ -438,7 +462,7 @@ struct BeamPlace {
         auto offer = [&](float x, int e) {
             if (x >= low) {
                 const double c = beam_value(sm, w, x);
-                if (c >= bound) f(c, static_cast<uint32_t>(w) * V + static_cast<uint32_t>(e));
+                if (c >= bound) f(c, (static_cast<uint32_t>(w) << kTokenBits) + static_cast<uint32_t>(e));
             }
         };
         if (ie >= 0) offer(xe, ie);
@@ -480,7 +504,7 @@ __device__ __forceinline__ bool beam_ended(const BeamParams& P, const BeamMergeS
 template <class F>
 __device__ __forceinline__ void beam_look_ended(const BeamParams& P, const BeamMergeSmem& sm, double bound, F f) {
     if (beam_ended(P, sm) && sm.s[threadIdx.x] >= bound)
-        f(sm.s[threadIdx.x], threadIdx.x * static_cast<uint32_t>(P.V) + static_cast<uint32_t>(P.eos));
+        f(sm.s[threadIdx.x], (threadIdx.x << kTokenBits) + static_cast<uint32_t>(P.eos));
 }
 
 // Every candidate of the n best tiles and the finished beams with a value of at
@@ -490,7 +514,7 @@ __device__ __forceinline__ void beam_visit(const BeamParams& P, int64_t b, int n
     BeamPlace<Tag, VEC> x;
     for (int i = threadIdx.x >> 5; i < n; i += NWARPS) {
         x.load(P, b, sm, i);
-        x.look(sm, static_cast<uint32_t>(P.V), bound, f);
+        x.look(sm, bound, f);
     }
     beam_look_ended(P, sm, bound, f);
 }
@@ -533,7 +557,8 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
     // sums are merged; rows that were not streamed hold nothing, what is read
     // there is not used.
     auto nth = [&](int j) { return j * NT + lane * NWARPS + ((wp + lane) & (NWARPS - 1)); };
-    const BeamStat first = beam_stat(P.stats + (b * P.W + min(wp, P.W - 1)) * P.segs, lane, P.segs);
+    BeamSegs first;
+    first.load(P.stats + (b * P.W + min(wp, P.W - 1)) * P.segs, 0, P.segs);
     float m[kMergePeaks];
 #pragma unroll
     for (int j = 0; j < kMergePeaks; ++j) {
@@ -555,7 +580,8 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
                 state = 2;
             } else {
                 const BeamStat* p = P.stats + r * P.segs;
-                const BeamStat a = beam_row_sum(p, P.segs, w == wp ? first : beam_stat(p, lane, P.segs));
+                if (w != wp) first.load(p, 0, P.segs);
+                const BeamStat a = beam_row_sum(p, P.segs, first);
                 if (!(a.S <= DBL_MAX)) {
                     bad = 1;  // a NaN or +inf logit
                 } else if (a.S > 0.0) {
@@ -569,6 +595,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
             sm.M[w] = M;
             sm.logS[w] = logS;
             sm.s[w] = static_cast<double>(s);
+            sm.add[w] = (static_cast<double>(s) - M) - logS;
             sm.state[w] = state;
         }
     }
@@ -583,8 +610,12 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
     // The tiles' values, and a bound that K of them reach: the K-th largest of
     // the 32 that the warps' 32 / NWARPS largest lanes make up (rounded down to
     // fp32).
+    // The row of tile i: the quotient is below 32 and its error below 2^-17, less
+    // than half a tile (at most 2^15 tiles a row).
+    const float inv = 1.0f / static_cast<float>(P.tiles);
+    auto row_of = [&](int i) { return static_cast<int>((static_cast<float>(i) + 0.5f) * inv); };
     auto value = [&](int i, float x) {
-        const int w = i / P.tiles;
+        const int w = row_of(i);
         return x > -INFINITY && sm.state[w] == 1 ? beam_value(sm, w, x) : -INFINITY;
     };
     double c[kMergePeaks], best = -INFINITY;
@@ -603,8 +634,9 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         if (!(v >= floor && v > -INFINITY)) return;
         const int at = atomicAdd(&sm.tiles, 1);
         if (at < kMergeTiles) {
+            const int w = row_of(i);
             sm.c[at] = v;
-            sm.id[at] = static_cast<uint32_t>(i);
+            sm.id[at] = (static_cast<uint32_t>(w) << kTileBits) + static_cast<uint32_t>(i - w * P.tiles);
         }
     };
 #pragma unroll
@@ -622,6 +654,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
             const double v = sm.c[i];
             const uint32_t id = sm.id[i];
             int rank = 0;
+#pragma unroll 4
             for (int j = 0; j < have; ++j) rank += beam_before(sm.c[j], sm.id[j], v, id) ? 1 : 0;
             if (rank < K) {
                 sm.tile_c[rank] = v;
@@ -654,8 +687,8 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
             if (has_y) e = fmax(e, y.best(sm));
             bound = fmax(bound, beam_bound(e, K, sm));
         }
-        if (has_x) x.look(sm, static_cast<uint32_t>(P.V), bound, take);
-        if (has_y) y.look(sm, static_cast<uint32_t>(P.V), bound, take);
+        if (has_x) x.look(sm, bound, take);
+        if (has_y) y.look(sm, bound, take);
         beam_look_ended(P, sm, bound, take);
     } else {
         if (few) bound = fmax(bound, beam_visit_bound<Tag, VEC>(P, b, n, sm));
@@ -708,6 +741,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
     for (int j = 0; j < kMergeCand / NT; ++j) {
         if (!(own_c[j] > -INFINITY)) continue;
         int rank = 0;
+#pragma unroll 4
         for (int i = 0; i < ranked; ++i) rank += beam_before(sm.c[i], sm.id[i], own_c[j], own_id[j]) ? 1 : 0;
         if (rank < K) beam_output(P, b * K + rank, own_c[j], own_id[j]);
     }
