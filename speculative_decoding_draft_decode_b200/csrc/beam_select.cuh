@@ -87,15 +87,17 @@ __device__ __forceinline__ uint4 minus_inf_vec() {
     return make_uint4(x, x, x, x);
 }
 
-// The K-th largest of the warp's 32 ordered values (INT_MIN: none).  Each lane
-// counts the values before its own.
-__device__ __forceinline__ int warp_kth(int p, int K) {
+// The K-th largest of 32 ordered values in shared memory (INT_MIN: none), for
+// every lane of the warp.  Each lane counts the values before its own.
+__device__ __forceinline__ int pool_kth(const int* pool, int K) {
     const int lane = threadIdx.x & 31;
+    const int p = pool[lane];
     int rank = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int x = __shfl_sync(FULL_MASK, p, i);
-        rank += x > p || (x == p && i < lane) ? 1 : 0;
+    for (int i = 0; i < 32; i += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(&pool[i]);
+        rank += (x.x > p || (x.x == p && i < lane) ? 1 : 0) + (x.y > p || (x.y == p && i + 1 < lane) ? 1 : 0) +
+                (x.z > p || (x.z == p && i + 2 < lane) ? 1 : 0) + (x.w > p || (x.w == p && i + 3 < lane) ? 1 : 0);
     }
     const unsigned who = __ballot_sync(FULL_MASK, rank == K - 1);
     return __shfl_sync(FULL_MASK, p, __ffs(who) - 1);
@@ -186,7 +188,7 @@ __device__ __forceinline__ float beam_end(const typename Tag::storage* row, cons
 __device__ __forceinline__ bool beam_far(float ref) { return !(fabsf(ref) < 1e37f); }
 __device__ __forceinline__ double beam_ref(float ref) {
     return beam_far(ref) ? static_cast<double>(ref)
-                         : static_cast<double>(__fmul_rn(ref, kLog2e)) / static_cast<double>(kLog2e);
+                         : static_cast<double>(__fmul_rn(ref, kLog2e)) * (1.0 / static_cast<double>(kLog2e));
 }
 __device__ __forceinline__ float beam_term(float x, float ref) {
     return ex2_sfu(beam_far(ref) ? (x - ref) * kLog2e : __fmaf_rn(x, kLog2e, -__fmul_rn(ref, kLog2e)));
@@ -195,41 +197,39 @@ __device__ __forceinline__ float beam_term(float x, float ref) {
 // The sum of a tile's terms, fp32: 2 x 16 (bf16) or 2 x 8 (fp32) of them.
 template <class Tag, int VEC>
 __device__ __forceinline__ float beam_sum(const uint4 (&w)[kTileU], float ref) {
-    if (beam_far(ref)) {
-        float s = 0.0f;
-#pragma unroll 1
-        for (int i = 0; i < kTileU * VEC; ++i) {
-            const int u = i / VEC;
-            const uint4 x = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
-            s += beam_term(VecOps<Tag, VEC>::elem(x, i % VEC), ref);
-        }
-        return s;
-    }
-    const float E = __fmul_rn(ref, kLog2e);
-    const uint64_t minus = f32x2(-E, -E), scale = f32x2(kLog2e, kLog2e);
+    const uint64_t scale = f32x2(kLog2e, kLog2e);
     uint64_t s = f32x2(0.0f, 0.0f);
+    auto sum = [&](auto exponent) {
 #pragma unroll
-    for (int u = 0; u < kTileU; ++u)
+        for (int u = 0; u < kTileU; ++u)
 #pragma unroll
-        for (int q = 0; q < VEC; q += 2) {
-            const uint64_t x = f32x2(VecOps<Tag, VEC>::elem(w[u], q), VecOps<Tag, VEC>::elem(w[u], q + 1));
-            const float2 e = f32x2_get(f32x2_fma(x, scale, minus));
-            s = f32x2_add(s, f32x2(ex2_sfu(e.x), ex2_sfu(e.y)));
-        }
+            for (int q = 0; q < VEC; q += 2) {
+                const float2 e = f32x2_get(exponent(f32x2(VecOps<Tag, VEC>::elem(w[u], q), VecOps<Tag, VEC>::elem(w[u], q + 1))));
+                s = f32x2_add(s, f32x2(ex2_sfu(e.x), ex2_sfu(e.y)));
+            }
+    };
+    if (beam_far(ref)) {
+        const uint64_t minus = f32x2(-ref, -ref), zero = f32x2(0.0f, 0.0f);
+        sum([&](uint64_t x) { return f32x2_fma(f32x2_add(x, minus), scale, zero); });
+    } else {
+        const float E = __fmul_rn(ref, kLog2e);
+        const uint64_t minus = f32x2(-E, -E);
+        sum([&](uint64_t x) { return f32x2_fma(x, scale, minus); });
+    }
     const float2 r = f32x2_get(s);
     return r.x + r.y;
 }
 
-// A tile's largest logit above the reference by more than this: the sum goes
-// over to it (terms stay below 2^6, far from overflow).
-constexpr float kBeamRaise = 4.0f;
+// The reference of values up to m: the multiple of 8 from m on, so that most
+// segments of a row share it and their sums add as they are.
+__device__ __forceinline__ float beam_up(float m) { return beam_far(m) ? fmaxf(m, -FLT_MAX) : 8.0f * ceilf(m * 0.125f); }
 
 // A sum over to another reference.
 __device__ __noinline__ double beam_carry(double S, float from, float to) {
     return S == 0.0 ? 0.0 : S * exp(beam_ref(from) - beam_ref(to));
 }
 
-// A warp's segment: tiles [t0, t1) of row r.
+// A warp's segment of row r.
 template <class Tag, int VEC>
 __device__ __forceinline__ void beam_stream(const BeamParams& P, int64_t r, int seg) {
     using Elem = typename Tag::storage;
@@ -239,6 +239,7 @@ __device__ __forceinline__ void beam_stream(const BeamParams& P, int64_t r, int 
     const RowCut cut = cut_row<Tag, VEC>(row, P.V);
     float* peaks = P.peaks + r * P.tiles;
     BeamTile<Tag, VEC> a;
+    if (!beam_streams(P, r)) return;  // warp-uniform
     a.load(row, cut, t0);
     int ie;
     const float xe = beam_end<Tag>(row, cut, P.V, t0 == 0, t1 == P.tiles, ie);
@@ -249,17 +250,18 @@ __device__ __forceinline__ void beam_stream(const BeamParams& P, int64_t r, int 
         if (tile == P.tiles - 1 && ie >= 0 && !is_head) m = fmaxf(m, xe);
         return from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(m)));
     };
-    float ref = fmaxf(peak(a.most(), t0), -FLT_MAX);
+    float ref = beam_up(peak(a.most(), t0));
     double S = 0.0;
     // The terms are summed while the tile's maximum is still on its way; a
-    // maximum far above the reference (rare) takes them again.
+    // maximum above the reference (rare) takes them again.
     auto take = [&](const BeamTile<Tag, VEC>& x, int tile) {
         const float m = peak(x.most(), tile);
         float s = beam_sum<Tag, VEC>(x.w, ref);
         if (lane == 0) peaks[tile] = m;
-        if (m > ref + kBeamRaise) {
-            S = beam_carry(S, ref, m);
-            ref = m;
+        if (m > ref) {
+            const float up = beam_up(m);
+            S = beam_carry(S, ref, up);
+            ref = up;
             s = beam_sum<Tag, VEC>(x.w, ref);
         }
         S += static_cast<double>(s);
@@ -297,7 +299,7 @@ struct BeamMergeSmem {
     uint32_t id[kMergeCand];    // their names
     double tile_c[kMaxBeams];   // the K best tiles
     uint32_t tile_id[kMaxBeams];
-    int pool[32];
+    __align__(16) int pool[32];
     double red_c[NWARPS];
     uint32_t red_id[NWARPS];
     int tiles, cands;
@@ -335,27 +337,27 @@ struct BeamSegs {
     }
 };
 
-// A row's sum from its segments' (x: the first 32 kSegs), each against about
-// the largest reference of those loaded with it.  Warp-collective.
+// A row's sum from its segments' (x: the first 32 kSegs), each against the
+// largest reference of those loaded with it.  Warp-collective.
 __device__ __forceinline__ BeamStat beam_row_sum(const BeamStat* p, int n, BeamSegs x) {
     BeamStat acc;
     acc.M = -DBL_MAX;
     acc.S = 0.0;
     for (int i0 = 0;;) {
-        float m = -FLT_MAX;
+        double M = -DBL_MAX;  // a segment's reference is an fp32 value's, so fp32 tells them apart
 #pragma unroll
         for (int j = 0; j < kSegs; ++j)
-            if (x.S[j] != 0.0) m = fmaxf(m, static_cast<float>(x.M[j]));
-        m = from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(m)));
-        double top = static_cast<double>(m);
+            if (x.S[j] != 0.0) M = fmax(M, x.M[j]);
+        const int o32 = ord_i32(static_cast<float>(M)), most = __reduce_max_sync(FULL_MASK, o32);
+        double top = __shfl_sync(FULL_MASK, M, __ffs(__ballot_sync(FULL_MASK, o32 == most)) - 1);
         if (acc.S != 0.0) top = fmax(top, acc.M);
         double S = 0.0;
 #pragma unroll
         for (int j = 0; j < kSegs; ++j)
-            if (x.S[j] != 0.0) S += x.S[j] * exp(x.M[j] - top);
+            if (x.S[j] != 0.0) S += x.M[j] != top ? x.S[j] * exp(x.M[j] - top) : x.S[j];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(FULL_MASK, S, o);
-        if (acc.S != 0.0) S += acc.S * exp(acc.M - top);
+        if (acc.S != 0.0) S += acc.M != top ? acc.S * exp(acc.M - top) : acc.S;
         acc.M = top;
         acc.S = S;
         i0 += 32 * kSegs;
@@ -455,10 +457,10 @@ struct BeamPlace {
     __device__ __forceinline__ void look(const BeamMergeSmem& sm, double bound, F f) const {
         const int lane = threadIdx.x & 31;
         // A logit below this has a value below the bound (the margin covers the
-        // rounding of the fp64 sums); what passes is compared in fp64.
-        const double at = (bound - sm.s[w]) + sm.logS[w] + sm.M[w];
-        const double slack = 1e-12 * (fabs(bound) + fabs(sm.s[w]) + fabs(sm.logS[w]) + fabs(sm.M[w]));
-        const float low = bound > -INFINITY ? fmaxf(__double2float_rd(at - slack), -FLT_MAX) : -FLT_MAX;
+        // roundings); what passes is compared in fp64.
+        const float at = __double2float_rd(bound - sm.add[w]);
+        const float slack = 1e-6f * (fabsf(at) + fabsf(static_cast<float>(bound)) + fabsf(static_cast<float>(sm.add[w])));
+        const float low = bound > -INFINITY ? fmaxf(at - slack, -FLT_MAX) : -FLT_MAX;
         auto offer = [&](float x, int e) {
             if (x >= low) {
                 const double c = beam_value(sm, w, x);
@@ -492,7 +494,7 @@ __device__ __forceinline__ double beam_bound(double best, int K, BeamMergeSmem& 
     }
     if (lane < kEach) sm.pool[wp * kEach + lane] = mine;
     __syncthreads();
-    const int kth = warp_kth(sm.pool[lane], K);
+    const int kth = pool_kth(sm.pool, K);
     __syncthreads();  // the pool may be written again
     return kth == INT_MIN ? -INFINITY : static_cast<double>(from_ord_i32(kth));
 }
@@ -546,31 +548,15 @@ __device__ __noinline__ void beam_many_candidates(const BeamParams& P, int64_t b
     }
 }
 
-// CTA-collective.
-template <class Tag, int VEC>
-__device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamMergeSmem& sm) {
-    const int t = threadIdx.x, lane = t & 31, wp = t >> 5;
-    const int K = P.K, total = P.W * P.tiles;
-    const float* peaks = P.peaks + b * total;
-    // Tile j of this thread: every warp gets tiles of all rows, so that the
-    // warps' best are the request's best.  The loads go out before the rows'
-    // sums are merged; rows that were not streamed hold nothing, what is read
-    // there is not used.
-    auto nth = [&](int j) { return j * NT + lane * NWARPS + ((wp + lane) & (NWARPS - 1)); };
-    BeamSegs first;
-    first.load(P.stats + (b * P.W + min(wp, P.W - 1)) * P.segs, 0, P.segs);
-    float m[kMergePeaks];
-#pragma unroll
-    for (int j = 0; j < kMergePeaks; ++j) {
-        const int i = nth(j);
-        m[j] = i < total ? __ldcg(&peaks[i]) : -INFINITY;
-    }
-    if (t == 0) sm.tiles = sm.cands = 0;
+// The rows' normalisers: sum(w) is the row's sum.  True (for the whole CTA) if
+// the request is undefined; its outputs are then written.
+template <class F>
+__device__ __forceinline__ bool beam_rows(const BeamParams& P, int64_t b, BeamMergeSmem& sm, F sum) {
+    const int lane = threadIdx.x & 31;
     int bad = 0;
-    for (int w = wp; w < P.W; w += NWARPS) {
-        const int64_t r = b * P.W + w;
-        const float s = __ldg(&P.scores[r]);
-        const bool fin = P.finished != nullptr && __ldg(&P.finished[r]) != 0;
+    for (int w = threadIdx.x >> 5; w < P.W; w += NWARPS) {
+        const float s = __ldg(&P.scores[b * P.W + w]);
+        const bool fin = P.finished != nullptr && __ldg(&P.finished[b * P.W + w]) != 0;
         int state = 0;
         double M = 0.0, logS = 0.0;
         if (!(s < INFINITY)) {
@@ -579,9 +565,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
             if (fin) {
                 state = 2;
             } else {
-                const BeamStat* p = P.stats + r * P.segs;
-                if (w != wp) first.load(p, 0, P.segs);
-                const BeamStat a = beam_row_sum(p, P.segs, first);
+                const BeamStat a = sum(w);
                 if (!(a.S <= DBL_MAX)) {
                     bad = 1;  // a NaN or +inf logit
                 } else if (a.S > 0.0) {
@@ -599,14 +583,92 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
             sm.state[w] = state;
         }
     }
-    if (__syncthreads_or(bad)) {
-        for (int i = t; i < K; i += NT) {
-            P.out_scores[b * K + i] = __uint_as_float(0x7fc00000u);
-            P.out_parents[b * K + i] = -1;
-            P.out_tokens[b * K + i] = -1;
-        }
-        return;
+    if (!__syncthreads_or(bad)) return false;
+    for (int i = threadIdx.x; i < P.K; i += NT) {
+        P.out_scores[b * P.K + i] = __uint_as_float(0x7fc00000u);
+        P.out_parents[b * P.K + i] = -1;
+        P.out_tokens[b * P.K + i] = -1;
     }
+    return true;
+}
+
+// The outputs from at most kMergeCand candidates in shared memory.
+__device__ __forceinline__ void beam_rank(const BeamParams& P, int64_t b, BeamMergeSmem& sm, int cands) {
+    const int t = threadIdx.x, K = P.K;
+    // A candidate's rank is its place.  Among many, those below the bound of
+    // the threads' best ones have none.
+    double own_c[kMergeCand / NT];
+    uint32_t own_id[kMergeCand / NT];
+    double e = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kMergeCand / NT; ++j) {
+        const int i = t + j * NT;
+        own_c[j] = -INFINITY;
+        own_id[j] = 0u;
+        if (i < cands) {
+            own_c[j] = sm.c[i];
+            own_id[j] = sm.id[i];
+            e = fmax(e, own_c[j]);
+        }
+    }
+    int ranked = cands;
+    if (cands > 64) {
+        const double least = beam_bound(e, K, sm);  // its barriers: every candidate has been read
+        if (t == 0) sm.cands = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kMergeCand / NT; ++j) {
+            if (!(own_c[j] >= least)) own_c[j] = -INFINITY;
+            if (own_c[j] > -INFINITY) {
+                const int at = atomicAdd(&sm.cands, 1);
+                sm.c[at] = own_c[j];
+                sm.id[at] = own_id[j];
+            }
+        }
+        __syncthreads();
+        ranked = sm.cands;
+    }
+#pragma unroll
+    for (int j = 0; j < kMergeCand / NT; ++j) {
+        if (!(own_c[j] > -INFINITY)) continue;
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < ranked; ++i) rank += beam_before(sm.c[i], sm.id[i], own_c[j], own_id[j]) ? 1 : 0;
+        if (rank < K) beam_output(P, b * K + rank, own_c[j], own_id[j]);
+    }
+    for (int i = cands + t; i < K; i += NT) {
+        P.out_scores[b * K + i] = -INFINITY;
+        P.out_parents[b * K + i] = -1;
+        P.out_tokens[b * K + i] = -1;
+    }
+}
+
+// CTA-collective.
+template <class Tag, int VEC>
+__device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamMergeSmem& sm) {
+    const int t = threadIdx.x, lane = t & 31, wp = t >> 5;
+    const int K = P.K, total = P.W * P.tiles;
+    const float* peaks = P.peaks + b * total;
+    // Tile j of this thread: every warp gets tiles of all rows, so that the
+    // warps' best are the request's best.  The loads go out before the rows'
+    // sums are merged; rows that were not streamed hold nothing, what is read
+    // there is not used.
+    auto nth = [&](int j) { return j * NT + lane * NWARPS + ((wp + lane) & (NWARPS - 1)); };
+    BeamSegs first;
+    first.load(P.stats + (b * P.W + min(wp, P.W - 1)) * P.segs, 0, P.segs);
+    float m[kMergePeaks];
+#pragma unroll
+    for (int j = 0; j < kMergePeaks; ++j) {
+        const int i = nth(j);
+        m[j] = j * NT < total && i < total ? __ldcg(&peaks[i]) : -INFINITY;
+    }
+    if (t == 0) sm.tiles = sm.cands = 0;
+    if (beam_rows(P, b, sm, [&](int w) {
+            const BeamStat* p = P.stats + (b * P.W + w) * P.segs;
+            if (w != wp) first.load(p, 0, P.segs);
+            return beam_row_sum(p, P.segs, first);
+        }))
+        return;
     // The tiles' values, and a bound that K of them reach: the K-th largest of
     // the 32 that the warps' 32 / NWARPS largest lanes make up (rounded down to
     // fp32).
@@ -621,8 +683,10 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
     double c[kMergePeaks], best = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kMergePeaks; ++j) {
+        c[j] = -INFINITY;
+        if (j * NT >= total) continue;  // CTA-uniform
         const int i = nth(j);
-        c[j] = i < total ? value(i, m[j]) : -INFINITY;
+        if (i < total) c[j] = value(i, m[j]);
         best = fmax(best, c[j]);
     }
     for (int j = kMergePeaks; j * NT < total; ++j) {
@@ -636,36 +700,44 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         if (at < kMergeTiles) {
             const int w = row_of(i);
             sm.c[at] = v;
-            sm.id[at] = (static_cast<uint32_t>(w) << kTileBits) + static_cast<uint32_t>(i - w * P.tiles);
+            const uint32_t id = (static_cast<uint32_t>(w) << kTileBits) + static_cast<uint32_t>(i - w * P.tiles);
+            sm.id[at] = id;
+            if (at < kMaxBeams) sm.tile_id[at] = id;
         }
     };
 #pragma unroll
-    for (int j = 0; j < kMergePeaks; ++j) keep(c[j], nth(j));
+    for (int j = 0; j < kMergePeaks; ++j)
+        if (j * NT < total) keep(c[j], nth(j));
     for (int j = kMergePeaks; j * NT < total; ++j) {
         const int i = nth(j);
         if (i < total) keep(value(i, __ldcg(&peaks[i])), i);
     }
     __syncthreads();
-    // The K best tiles, a tile's rank being its place.
+    // Few enough tiles to hold in registers are all taken; of more the K best, a
+    // tile's rank being its place.
     const int have = sm.tiles;
-    int n = min(have, K);
-    if (have <= kMergeTiles) {
-        for (int i = t; i < have; i += NT) {
-            const double v = sm.c[i];
-            const uint32_t id = sm.id[i];
-            int rank = 0;
+    int n = have;
+    double bound = floor;
+    if (have > 2 * NWARPS) {
+        n = min(have, K);
+        if (have <= kMergeTiles) {
+            for (int i = t; i < have; i += NT) {
+                const double v = sm.c[i];
+                const uint32_t id = sm.id[i];
+                int rank = 0;
 #pragma unroll 4
-            for (int j = 0; j < have; ++j) rank += beam_before(sm.c[j], sm.id[j], v, id) ? 1 : 0;
-            if (rank < K) {
-                sm.tile_c[rank] = v;
-                sm.tile_id[rank] = id;
+                for (int j = 0; j < have; ++j) rank += beam_before(sm.c[j], sm.id[j], v, id) ? 1 : 0;
+                if (rank < K) {
+                    sm.tile_c[rank] = v;
+                    sm.tile_id[rank] = id;
+                }
             }
+        } else {
+            n = beam_many_tiles(P, peaks, sm);
         }
-    } else {
-        n = beam_many_tiles(P, peaks, sm);
+        __syncthreads();
+        bound = n == K ? sm.tile_c[K - 1] : -INFINITY;
     }
-    __syncthreads();
-    double bound = n == K ? sm.tile_c[K - 1] : -INFINITY;
     auto take = [&](double v, uint32_t id) {
         const int at = atomicAdd(&sm.cands, 1);
         if (at < kMergeCand) {
@@ -704,52 +776,8 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         __syncthreads();
         cands = sm.cands;
     }
-    if (cands > kMergeCand) {
-        beam_many_candidates<Tag, VEC>(P, b, n, bound, sm);
-        return;
-    }
-    // A candidate's rank is its place.  Among many, those below the bound of
-    // the threads' best ones have none.
-    double own_c[kMergeCand / NT];
-    uint32_t own_id[kMergeCand / NT];
-    double e = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kMergeCand / NT; ++j) {
-        const int i = t + j * NT;
-        own_c[j] = i < cands ? sm.c[i] : -INFINITY;
-        own_id[j] = i < cands ? sm.id[i] : 0u;
-        e = fmax(e, own_c[j]);
-    }
-    int ranked = cands;
-    if (cands > 64) {
-        const double least = beam_bound(e, K, sm);  // its barriers: every candidate has been read
-        if (t == 0) sm.cands = 0;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kMergeCand / NT; ++j) {
-            if (!(own_c[j] >= least)) own_c[j] = -INFINITY;
-            if (own_c[j] > -INFINITY) {
-                const int at = atomicAdd(&sm.cands, 1);
-                sm.c[at] = own_c[j];
-                sm.id[at] = own_id[j];
-            }
-        }
-        __syncthreads();
-        ranked = sm.cands;
-    }
-#pragma unroll
-    for (int j = 0; j < kMergeCand / NT; ++j) {
-        if (!(own_c[j] > -INFINITY)) continue;
-        int rank = 0;
-#pragma unroll 4
-        for (int i = 0; i < ranked; ++i) rank += beam_before(sm.c[i], sm.id[i], own_c[j], own_id[j]) ? 1 : 0;
-        if (rank < K) beam_output(P, b * K + rank, own_c[j], own_id[j]);
-    }
-    for (int i = cands + t; i < K; i += NT) {
-        P.out_scores[b * K + i] = -INFINITY;
-        P.out_parents[b * K + i] = -1;
-        P.out_tokens[b * K + i] = -1;
-    }
+    if (cands > kMergeCand) beam_many_candidates<Tag, VEC>(P, b, n, bound, sm);
+    else beam_rank(P, b, sm, cands);
 }
 
 // Rows of many tiles: a warp per segment, then a CTA per request.  The second
@@ -763,7 +791,7 @@ __global__ void __launch_bounds__(NT, 5) beam_pass_kernel(const BeamParams P) {
     grid_launch_dependents();
     const unsigned unit = blockIdx.x * NWARPS + (threadIdx.x >> 5);
     const unsigned r = unit / static_cast<unsigned>(P.segs);
-    if (r >= static_cast<unsigned>(P.B * P.W) || !beam_streams(P, r)) return;  // warp-uniform; no CTA barrier below
+    if (r >= static_cast<unsigned>(P.B * P.W)) return;  // warp-uniform; no CTA barrier below
     beam_stream<Tag, VEC>(P, r, static_cast<int>(unit - r * static_cast<unsigned>(P.segs)));
 }
 
@@ -775,20 +803,96 @@ __global__ void __launch_bounds__(NT, 2) beam_merge_kernel(const BeamParams P) {
     beam_merge<Tag, VEC>(P, blockIdx.x, sm);
 }
 
-// Requests of at most kSmallTiles tiles: one CTA does both, in one launch.
-constexpr int kSmallTiles = 32;
+// Requests of at most kSmallTiles tiles: one CTA and one launch.  Every tile
+// stays in its warp's registers from the first read to the last, so there is
+// nothing to select tiles for.
+constexpr int kSmallTiles = 2 * NWARPS;
+
+struct BeamSmallSmem : BeamMergeSmem {
+    BeamStat stat[kSmallTiles];
+};
+
 template <class Tag, int VEC>
 __global__ void __launch_bounds__(NT, 2) beam_small_kernel(const BeamParams P) {
-    __shared__ BeamMergeSmem sm;
+    __shared__ BeamSmallSmem sm;
+    const int t = threadIdx.x, lane = t & 31, wp = t >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t b = blockIdx.x;
-    for (int unit = threadIdx.x >> 5; unit < P.W * P.segs; unit += NWARPS) {
-        const int w = unit / P.segs;
-        if (beam_streams(P, b * P.W + w)) beam_stream<Tag, VEC>(P, b * P.W + w, unit - w * P.segs);
-    }
+    const int units = P.W * P.tiles;  // unit u: tile u % tiles of beam u / tiles
+    if (t == 0) sm.cands = 0;
+    if (t < kSmallTiles) sm.tile_id[t] = static_cast<uint32_t>(t / P.tiles << kTileBits) + static_cast<uint32_t>(t % P.tiles);
     __syncthreads();
-    beam_merge<Tag, VEC>(P, b, sm);
+    BeamPlace<Tag, VEC> x, y;
+    bool has_x = wp < units, has_y = wp + NWARPS < units;
+    // Loaded before it is known whether the rows are streamed.
+    if (has_x) x.load(P, b, sm, wp);
+    if (has_y) y.load(P, b, sm, wp + NWARPS);
+    has_x = has_x && beam_streams(P, b * P.W + x.w);
+    has_y = has_y && beam_streams(P, b * P.W + y.w);
+    auto total = [&](const BeamPlace<Tag, VEC>& p, int u) {
+        const float ref = beam_up(from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(fmaxf(p.a.most(), p.xe)))));
+        double S = static_cast<double>(beam_sum<Tag, VEC>(p.a.w, ref));
+        if (p.ie >= 0) S += static_cast<double>(beam_term(p.xe, ref));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(FULL_MASK, S, o);
+        if (lane == 0) {
+            sm.stat[u].M = beam_ref(ref);
+            sm.stat[u].S = S;
+        }
+    };
+    if (has_x) total(x, wp);
+    if (has_y) total(y, wp + NWARPS);
+    __syncthreads();
+    if (beam_rows(P, b, sm, [&](int w) {
+            BeamSegs v;
+#pragma unroll
+            for (int j = 0; j < kSegs; ++j) {
+                v.M[j] = -DBL_MAX;
+                v.S[j] = 0.0;
+            }
+            if (lane < P.tiles) {
+                v.M[0] = sm.stat[w * P.tiles + lane].M;
+                v.S[0] = sm.stat[w * P.tiles + lane].S;
+            }
+            return beam_row_sum(nullptr, P.tiles, v);
+        }))
+        return;
+    has_x = has_x && sm.state[x.w] == 1;  // a row of only -inf holds no candidate
+    has_y = has_y && sm.state[y.w] == 1;
+    double e = beam_ended(P, sm) ? sm.s[t] : -INFINITY;
+    if (has_x) e = fmax(e, x.best(sm));
+    if (has_y) e = fmax(e, y.best(sm));
+    const double bound = beam_bound(e, P.K, sm);
+    auto take = [&](double v, uint32_t id) {
+        const int at = atomicAdd(&sm.cands, 1);
+        if (at < kMergeCand) {
+            sm.c[at] = v;
+            sm.id[at] = id;
+        }
+    };
+    if (has_x) x.look(sm, bound, take);
+    if (has_y) y.look(sm, bound, take);
+    beam_look_ended(P, sm, bound, take);
+    __syncthreads();
+    const int cands = sm.cands;
+    if (cands <= kMergeCand) {
+        beam_rank(P, b, sm, cands);
+        return;
+    }
+    // Runs of equal values: the best one behind the last one found, K times.
+    BeamBest last = {INFINITY, 0u};
+    for (int i = 0; i < P.K; ++i) {
+        BeamBest best = {-INFINITY, 0xffffffffu};
+        auto offer = [&](double c, uint32_t id) {
+            if (beam_before(last.c, last.id, c, id) && beam_before(c, id, best.c, best.id)) best = {c, id};
+        };
+        if (has_x) x.look(sm, bound, offer);
+        if (has_y) y.look(sm, bound, offer);
+        beam_look_ended(P, sm, bound, offer);
+        last = beam_block_best(best, sm);
+        if (t == 0) beam_output(P, b * P.K + i, last.c, last.id);
+    }
 }
 
 }  // namespace specdec

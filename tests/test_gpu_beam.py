@@ -1,13 +1,14 @@
 """Beam selection on the GPU against the plain 64-bit reference.
 
 Tolerance of a score, from the kernel's arithmetic.  Its own rounding to fp32
-is at most half a step: 2^-24 |score|.  The row sum S = sum exp(l - M) carries,
-relative to S: ex2.approx 2^-22; the fp32 sum of the up to 8 elements of a
-vector 7 * 2^-24; and in the exponent d = l - M three roundings (the
-difference, log2 e and the product, 2.5 * 2^-24 relative), which weigh
-2.5 * 2^-24 sum p |d| <= 2.5 * 2^-24 log V (|d| = -log p - log S, so the
-weighted sum is at most the entropy) <= 2.5 * 2^-24 * 16.7.  Together below
-2.4e-7 + 4.2e-7 + 2.5e-6 < 4e-6, which log S carries as an absolute error.
+is at most half a step: 2^-24 |score|.  The row sum S = sum exp(l - ref) carries,
+relative to S: ex2.approx 2^-22; the fp32 sum of the up to 32 elements of a
+lane's tile, 17 * 2^-24; and in the exponent d = l - ref one rounding of l c - E
+(2^-24 relative) and that of c = log2 e in fp32 (2^-26), which weigh 1.25 * 2^-24
+sum p |d|.  The reference lies up to 8 above the largest logit, and the rest of
+|d| = -log p - log S weighs at most the entropy, log V <= 16.7: 1.25 * 2^-24 *
+24.7.  Together below 2.4e-7 + 1.02e-6 + 1.85e-6 < 4e-6, which log S carries as
+an absolute error.
 Two candidates of different beams whose values are more than twice that apart
 are in the reference's order; candidates of one beam always are."""
 import numpy as np
@@ -181,6 +182,32 @@ def test_undefined_requests(torch_, ver):
         s[3, 1] = np.inf
         x[4, 0] = np.nan
         check(torch_, ver, x, s, 4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_crowded_tiles(torch_, ver, dtype):
+    """Real vocabularies are not shuffled: the likely tokens stand together, so
+    one tile holds many more candidates than K, or all of them; and rows whose
+    logits are far from zero."""
+    rng = np.random.default_rng(17)
+    for V, K in ((6000, 8), (40000, 32)):
+        x = rng.standard_normal((4, 3, V)).astype(np.float32)
+        x[0] += np.linspace(30, 0, V)[None]          # falling with the index
+        x[1, :, 1000:2100] += 9.0                    # one crowded stretch
+        x[2] += 900.0
+        x[3] = x[3] * 1e-3 - 5e4
+        check(torch_, ver, x, beam_scores(rng, 4, 3), K, dtype)
+
+
+def test_huge_logits(torch_, ver):
+    """Values near the ends of fp32, where the reference times log2 e overflows."""
+    rng = np.random.default_rng(18)
+    x = rng.standard_normal((3, 2, 9000)).astype(np.float32)
+    x[0] = x[0] * 2e37
+    x[1] = -3.0e38 + np.abs(x[1]) * 1e37
+    x[2, 0] = np.float32(2.0e37)
+    x[2, 1] = -np.float32(2.0e37)
+    check(torch_, ver, x, beam_scores(rng, 3, 2), 6)
 
 
 def test_large_vocabulary(torch_, ver):

@@ -97,6 +97,32 @@ def test_reorder_far_strides(torch_, sd_):
     assert np.array_equal(host(x), ref.reorder_states(src, src, par, None))
 
 
+@pytest.mark.parametrize("T,D", [(29, 33), (200, 7), (9, 255), (16, 8)])
+@pytest.mark.parametrize("first,gap", [(0, 0), (1, 0), (3, 5), (7, 16)])
+def test_reorder_odd_runs(torch_, sd_, T, D, first, gap):
+    """2-byte rows of odd size at odd addresses, out of place: every phase of a
+    beam's run against 16 bytes, with the bytes around the runs left alone."""
+    torch = torch_
+    rng = np.random.default_rng(T + first)
+    G, B, W = 2, 3, 7
+    run = T * D + gap
+    n = first + G * B * W * run + 40
+
+    def view(buf):
+        return torch.as_strided(buf, (G, B, W, T, D), (B * W * run, W * run, run, D, 1), first)
+
+    src = torch.from_numpy(rng.integers(-30000, 30000, n).astype(np.int16)).cuda()
+    dst = torch.from_numpy(rng.integers(-30000, 30000, n).astype(np.int16)).cuda()
+    par, lens = parents_of(rng, B, W), np.array([T, T // 2, 1], np.int32)
+    old, flat = host(view(dst)).copy(), host(dst).copy()
+    sd_.reorder_states(view(src), torch.from_numpy(par).cuda(), torch.from_numpy(lens).cuda(), out=view(dst))
+    want = ref.reorder_states(host(view(src)), old, par, lens)
+    assert np.array_equal(host(view(dst)), want)
+    again = torch.from_numpy(flat).cuda()
+    view(again).copy_(torch.from_numpy(want))
+    assert np.array_equal(host(dst), host(again))
+
+
 def test_reorder_many_items(torch_, sd_):
     """More work items than resident CTAs, ragged: every item is taken."""
     torch = torch_
