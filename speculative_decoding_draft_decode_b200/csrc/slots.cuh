@@ -152,7 +152,9 @@ __device__ __forceinline__ void plan_move(const PlanParams& P, const PlanMove& m
     }
 }
 
-constexpr int kPlanOwn = 4;  // pages that a thread moves by itself; longer moves are shared by its warp
+// Pages that a thread takes or returns by itself, one after another; the few
+// longer moves (prompts, released requests) are shared by its warp.
+constexpr int kPlanTake = 12, kPlanReturn = 4;
 
 struct PlanSmem {
     PlanScan warp[kPlanThreads / 32];
@@ -246,8 +248,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_tables_kernel(const PlanPar
             }
         }
         const int pages = b < P.B ? (m.got > 0 ? m.got : q.back) : 0;
-        if (pages > 0 && pages <= kPlanOwn) plan_move(P, m, head, count, 0, 1);
-        for (unsigned long_ones = __ballot_sync(FULL_MASK, pages > kPlanOwn); long_ones != 0u; long_ones &= long_ones - 1u) {
+        const bool own = pages <= (m.got > 0 ? kPlanTake : kPlanReturn);
+        if (pages > 0 && own) plan_move(P, m, head, count, 0, 1);
+        for (unsigned long_ones = __ballot_sync(FULL_MASK, !own); long_ones != 0u; long_ones &= long_ones - 1u) {
             const int l = __ffs(long_ones) - 1;
             PlanMove x;
             x.b = __shfl_sync(FULL_MASK, m.b, l);

@@ -74,7 +74,7 @@ def test_fixed_layout(torch_, sd_, B, k, bs, in_place):
     check(torch_, sd_, lens, tables, held, ring, state, bs, k)
 
 
-@pytest.mark.parametrize("B", [1, 20, 1500])
+@pytest.mark.parametrize("B", [1, 20, 1500, 8192, 8200])
 def test_packed_layout(torch_, sd_, B):
     rng = np.random.default_rng(B)
     k, bs = 8, 16
@@ -157,13 +157,26 @@ def test_fresh_outputs_and_refusals(torch_, sd_):
             sd_.plan_slots(**{**a, **bad})
 
 
-def test_steps_in_a_graph(torch_, sd_):
+def test_uneven_rows(torch_, sd_):
+    """Packed drafts that stand close together: one CTA's requests have most of
+    the rows, more than it maps at a time."""
+    rng = np.random.default_rng(21)
+    for B in (1024, 3000):
+        n = np.zeros(B, np.int64)
+        n[5:505] = rng.integers(10, 32, 500)
+        off = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        lens, tables, held, ring, state = requests(rng, B, 16, 12, 3 * B, 100)
+        check(torch_, sd_, lens, tables, held, ring, state, 16, 32, off, int(off[-1]))
+
+
+@pytest.mark.parametrize("B", [50, 1500])
+def test_steps_in_a_graph(torch_, sd_, B):
     """A decode loop's planning captured once and replayed: lengths, pages and
     the ring move on in place, step after step."""
     torch = torch_
     rng = np.random.default_rng(8)
-    B, k, bs, cols = 50, 4, 8, 40
-    lens, tables, held, ring, state = requests(rng, B, bs, cols, 700, 40)
+    k, bs, cols = 4, 8, 40
+    lens, tables, held, ring, state = requests(rng, B, bs, cols, 14 * B, 40)
     dev = lambda a: torch.from_numpy(a.copy()).cuda()  # noqa: E731
     t = dict(seq_lens=dev(lens), block_tables=dev(tables), held_blocks=dev(held), free_ring=dev(ring), ring_state=dev(state))
     accept, release = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
