@@ -432,7 +432,8 @@ specdec_status specdec_ngram_propose(const int32_t* tokens, int64_t token_stride
  *                beam_scores[w]; its row is not read.  eos_token in [0, V) is
  *                checked when finished is given.
  *   out_scores   [B, K] float32, descending; out_parents, out_tokens [B, K]
- *                int32: the beam w and the token v of each
+ *                int32: the beam w and the token v of each.  With K == W
+ *                out_scores may be beam_scores
  * A logit of -inf is no candidate; with fewer than K candidates the rest is
  * (-inf, -1, -1).  A request with a score of NaN or +inf, or with a NaN or
  * +inf logit in a row that is read, gets scores NaN, parents and tokens -1.

@@ -131,7 +131,7 @@ def test_equal_values(torch_, ver, dtype, K):
     """Ties go to the lowest w V + v: rows of one value, of few values, of
     signed zeros; more ties than any buffer holds."""
     rng = np.random.default_rng(3)
-    for V in (40, 3000, 20480):
+    for V in (40, 1000, 3000, 20480):
         x = np.zeros((5, 4, V), np.float32)
         x[1] = rng.integers(0, 2, (4, V))
         x[2] = np.where(rng.random((4, V)) < 0.5, -0.0, 0.0)
@@ -250,6 +250,40 @@ def test_out_streams_and_graphs(torch_, ver):
         s.copy_(torch.from_numpy(ss[i].astype(np.float32)))
         graph.replay()
         compare([host(a) for a in out], xs[i].astype(np.float64), ss[i].astype(np.float32).astype(np.float64), K)
+
+
+def test_scores_in_place_and_stream_handles(torch_, ver):
+    """The new scores may go where the old ones were (as many beams selected as
+    there were); a stream may be given by its handle."""
+    torch = torch_
+    rng = np.random.default_rng(6)
+    for B, W, V in ((3, 4, 500), (2, 9, 30000)):
+        x, s = logits(rng, B, W, V), beam_scores(rng, B, W).astype(np.float32)
+        t, old = torch.from_numpy(x).cuda(), torch.from_numpy(s).cuda()
+        out = (old, torch.empty(B, W, dtype=torch.int32, device="cuda"), torch.empty(B, W, dtype=torch.int32, device="cuda"))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        ver.beam_select(t, old, W, out=out, stream=side.cuda_stream)
+        compare([host(a) for a in out], x.astype(np.float64), s.astype(np.float64), W)
+
+
+def test_many_requests(torch_, ver):
+    """The largest batch, in one launch and in two."""
+    torch = torch_
+    g = torch.Generator("cuda")
+    g.manual_seed(9)
+    for W, V in ((2, 40), (20, 24)):
+        x = torch.randn((65536, W, V), generator=g, device="cuda")
+        s = -torch.rand((65536, W), generator=g, device="cuda")
+        got = ver.beam_select(x, s, 2)
+        c = (torch.log_softmax(x.double(), 2) + s.double()[..., None]).flatten(1)
+        want, at = c.topk(2, 1)
+        clear = (want[:, 0] - want[:, 1] > 8e-6) & (want[:, 1] - c.topk(3, 1).values[:, 2] > 8e-6)
+        assert (got[0] - want).abs().max() < 4e-6 + 2.0**-24 * 20
+        assert torch.equal(got[1][clear], (at // V).int()[clear]) and torch.equal(got[2][clear], (at % V).int()[clear])
+        assert clear.float().mean() > 0.99
+    with pytest.raises(Exception):
+        ver.beam_select(torch.zeros(65537, 1, 4, device="cuda"), torch.zeros(65537, 1, device="cuda"), 1)
 
 
 def test_shares_a_workspace_with_the_verifier(torch_, ver):

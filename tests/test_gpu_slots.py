@@ -62,7 +62,7 @@ def check(torch, sd, lens, tables, held, ring, state, bs, k=0, offsets=None, tot
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("B,k,bs", [(1, 0, 1), (3, 4, 16), (64, 5, 16), (33, 64, 48), (500, 32, 8), (1024, 3, 64), (1025, 2, 16),
-                                    (5000, 1, 16), (9000, 7, 4)])
+                                    (5000, 1, 16), (9000, 7, 4), (65536, 0, 16)])
 def test_fixed_layout(torch_, sd_, B, k, bs, in_place):
     rng = np.random.default_rng(B + k)
     max_len = 300

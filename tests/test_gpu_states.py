@@ -136,6 +136,25 @@ def test_reorder_many_items(torch_, sd_):
     assert np.array_equal(host(got), ref.reorder_states(host(x), np.zeros(x.shape, np.int16), par, lens))
 
 
+@pytest.mark.parametrize("shape", [(70000, 1, 2, 3, 4), (1, 65536, 2, 2, 2), (3, 2, 5, 11)])
+def test_reorder_large_counts(torch_, sd_, shape):
+    """More groups or requests than a grid has rows; token histories (a position
+    is one element)."""
+    torch = torch_
+    rng = np.random.default_rng(shape[1])
+    src, old = bits(rng, shape, "f32"), bits(rng, shape, "f32")
+    par = parents_of(rng, shape[1], shape[2])
+    x, to = torch.from_numpy(src).cuda(), torch.from_numpy(old).cuda()
+    sd_.reorder_states(x, torch.from_numpy(par).cuda(), out=to)
+    ok = (par >= 0) & (par < shape[2])
+    idx = np.where(ok, par, 0)
+    moved = src[:, np.arange(shape[1])[:, None], idx]
+    keep = ok.reshape(1, *par.shape, *([1] * (len(shape) - 3)))
+    assert np.array_equal(host(to), np.where(keep, moved, old))
+    sd_.reorder_states(x, torch.from_numpy(par).cuda())
+    assert np.array_equal(host(x), np.where(keep, moved, src))
+
+
 def test_reorder_graph_and_stream(torch_, sd_):
     torch = torch_
     rng = np.random.default_rng(6)
@@ -231,6 +250,25 @@ def test_commit_in_place(torch_, sd_, N, depth, row):
     want = ref.commit_path(cache, al, nodes, host(z), slots + 2, slots)
     sd_.commit_path(y, dev(al), dev(nodes), z, dev(slots + 2), src_slots=sl)
     assert np.array_equal(host(z), want) and np.array_equal(host(y), cache)
+
+
+@pytest.mark.parametrize("G,B", [(70000, 1), (1, 65536)])
+def test_commit_large_counts(torch_, sd_, G, B):
+    torch = torch_
+    rng = np.random.default_rng(G)
+    src, cache = bits(rng, (G, B, 3, 2), "f32"), bits(rng, (G, 2 * B + 3, 2), "f32")
+    al = rng.integers(-1, 2, B).astype(np.int32)
+    nodes = rng.integers(1, 3, (B, 1)).astype(np.int32)
+    slots = rng.permutation(2 * B + 3)[:2 * B].reshape(B, 2).astype(np.int64)
+    to = torch.from_numpy(cache.copy()).cuda()
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    sd_.commit_path(dev(src), dev(al), dev(nodes), to, dev(slots))
+    want = cache.copy()
+    b = np.nonzero(al >= 0)[0]
+    want[:, slots[b, 0]] = src[:, b, 0]
+    b = np.nonzero(al >= 1)[0]
+    want[:, slots[b, 1]] = src[:, b, nodes[b, 0]]
+    assert np.array_equal(host(to), want)
 
 
 def test_commit_refusals(torch_, sd_):
