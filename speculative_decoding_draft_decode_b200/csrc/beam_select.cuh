@@ -7,15 +7,19 @@
 //   c = s_w + l_wv - log sum_v' exp(l_wv'),
 // and the K largest are kept, equal values in order of w V + v.
 //
-// beam_stream reads the logits once.  A warp takes a segment of a row,
-// tile by tile (128 vectors of 16 bytes, 4 a lane, loaded one tile ahead), and
-// keeps sum exp(l - ref) and every tile's largest logit.  Nothing is selected
-// here, so warps need neither thresholds nor one another.
-// beam_merge, one CTA per request: the rows' sums, then the K best
-// tiles by (c of the largest logit, position).  An element of any other tile
-// has K elements before it (the largest ones of these K tiles: greater, or
-// equal and earlier), so only K tiles are read again.  Values are ordered in
-// fp64.  Every sum has a fixed order: results do not vary from run to run.
+// beam_stream reads the logits once.  A warp takes a segment of a row, tile by
+// tile (128 vectors of 16 bytes, 4 a lane), and keeps sum exp(l - ref) and every
+// tile's largest logit.  Nothing is selected here, so warps need neither
+// thresholds nor one another.  Bound by load latency together with the
+// special-function unit: 64 x 8 rows of 128256 bf16 take 26.5 us (5.0 TB/s), the
+// same with 4 to 6 CTAs per SM, with a tile loaded ahead, or with part of the
+// exponentials as polynomials.
+// beam_merge, one CTA per request: the rows' sums, then the K best tiles by (c
+// of the largest logit, position).  An element of any other tile has K elements
+// before it (the largest ones of these K tiles: greater, or equal and earlier),
+// so only K tiles are read again (up to 16 if that many reach the bound).  Values
+// are ordered in fp64.  About 5 us, a chain of dependent steps.  Every sum has a
+// fixed order: results do not vary from run to run.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -194,9 +198,19 @@ __device__ __forceinline__ float beam_term(float x, float ref) {
     return ex2_sfu(beam_far(ref) ? (x - ref) * kLog2e : __fmaf_rn(x, kLog2e, -__fmul_rn(ref, kLog2e)));
 }
 
+// A reference as the sums use it.
+struct BeamRef {
+    uint64_t minus;  // -E, or -ref where that is far, twice
+    bool far;
+    __device__ __forceinline__ explicit BeamRef(float ref) : far(beam_far(ref)) {
+        const float x = far ? -ref : -__fmul_rn(ref, kLog2e);
+        minus = f32x2(x, x);
+    }
+};
+
 // The sum of a tile's terms, fp32: 2 x 16 (bf16) or 2 x 8 (fp32) of them.
 template <class Tag, int VEC>
-__device__ __forceinline__ float beam_sum(const uint4 (&w)[kTileU], float ref) {
+__device__ __forceinline__ float beam_sum(const uint4 (&w)[kTileU], const BeamRef& ref) {
     const uint64_t scale = f32x2(kLog2e, kLog2e);
     uint64_t s = f32x2(0.0f, 0.0f);
     auto sum = [&](auto exponent) {
@@ -208,13 +222,11 @@ __device__ __forceinline__ float beam_sum(const uint4 (&w)[kTileU], float ref) {
                 s = f32x2_add(s, f32x2(ex2_sfu(e.x), ex2_sfu(e.y)));
             }
     };
-    if (beam_far(ref)) {
-        const uint64_t minus = f32x2(-ref, -ref), zero = f32x2(0.0f, 0.0f);
-        sum([&](uint64_t x) { return f32x2_fma(f32x2_add(x, minus), scale, zero); });
+    if (ref.far) {
+        const uint64_t zero = f32x2(0.0f, 0.0f);
+        sum([&](uint64_t x) { return f32x2_fma(f32x2_add(x, ref.minus), scale, zero); });
     } else {
-        const float E = __fmul_rn(ref, kLog2e);
-        const uint64_t minus = f32x2(-E, -E);
-        sum([&](uint64_t x) { return f32x2_fma(x, scale, minus); });
+        sum([&](uint64_t x) { return f32x2_fma(x, scale, ref.minus); });
     }
     const float2 r = f32x2_get(s);
     return r.x + r.y;
@@ -286,33 +298,29 @@ __device__ __forceinline__ void beam_stream(const BeamParams& P, int64_t r, int 
     a.load(row, cut, t0);
     int ie;
     const float xe = beam_end<Tag>(row, cut, P.V, t0 == 0, t1 == P.tiles, ie);
+    // A head element counts to the segment's first tile's largest logit, a tail
+    // element to the last one's.
     const bool is_head = ie >= 0 && ie < cut.head;
-    // The largest logit of a tile, for all lanes.
-    auto peak = [&](float m, int tile) {
-        if (tile == 0 && is_head) m = fmaxf(m, xe);
-        if (tile == P.tiles - 1 && ie >= 0 && !is_head) m = fmaxf(m, xe);
-        return from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(m)));
-    };
-    float ref = beam_up(peak(a.most(), t0));
+    const float x0 = is_head ? xe : -INFINITY, x1 = is_head ? -INFINITY : xe;
+    auto warp_max = [](float m) { return from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(m))); };
+    float m = warp_max(fmaxf(fmaxf(a.most(), x0), t0 + 1 == t1 ? x1 : -INFINITY));
+    float ref = beam_up(m);
+    BeamRef use(ref);
     double S = 0.0;
-    // The terms are summed while the tile's maximum is still on its way; a
-    // maximum above the reference (rare) takes them again.
-    auto take = [&](const BeamTile<Tag, VEC>& x, int tile) {
-        const float m = peak(x.most(), tile);
-        float s = beam_sum<Tag, VEC>(x.w, ref);
-        if (lane == 0) peaks[tile] = m;
-        if (m > ref) {
+    for (int t = t0;;) {
+        float s = beam_sum<Tag, VEC>(a.w, use);
+        if (lane == 0) peaks[t] = m;
+        if (m > ref) {  // rare: the terms again, against a new reference
             const float up = beam_up(m);
             S = beam_carry(S, ref, up);
             ref = up;
-            s = beam_sum<Tag, VEC>(x.w, ref);
+            use = BeamRef(ref);
+            s = beam_sum<Tag, VEC>(a.w, use);
         }
         S += static_cast<double>(s);
-    };
-    for (int t = t0;;) {
-        take(a, t);
         if (++t >= t1) break;
         a.load(row, cut, t);
+        m = warp_max(t + 1 == t1 ? fmaxf(a.most(), x1) : a.most());  // on its way while the terms are summed
     }
     if (ie >= 0) S += static_cast<double>(beam_term(xe, ref));
     S = warp_sum_f64(S);
@@ -482,9 +490,9 @@ __device__ __noinline__ int beam_many_tiles(const BeamParams& P, const float* pe
 // of 1e-7; one of 128256 errs by 7e-9 without, and mending would cost a merge
 // 2.9 us (14.6 against 11.7 us at 16 x 4 rows of 128256 bf16).
 constexpr int kMendTiles = 16;
-// Bounds taken before that are lowered by this much (a sum's error is below
-// 4e-6).
-constexpr double kMendSlack = 1e-5;
+// Bounds taken before that are lowered by more than values can fall with it (a
+// sum's error is below 4e-6, and a value's last place moves).
+__device__ __forceinline__ double beam_slack(double bound) { return bound - (1e-5 + 1e-14 * fabs(bound)); }
 
 // One of the K best tiles, as a warp reads it again.
 template <class Tag, int VEC>
@@ -517,7 +525,7 @@ struct BeamPlace {
         const float m = __shfl_sync(FULL_MASK, p, tile - t0);
         const float ref = beam_up(from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(p))));
         if (beam_far(ref)) return;
-        double d = beam_sum_exact<Tag, VEC>(a.w, a.most(), ref, m - kBeamLarge) - static_cast<double>(beam_sum<Tag, VEC>(a.w, ref));
+        double d = beam_sum_exact<Tag, VEC>(a.w, a.most(), ref, m - kBeamLarge) - static_cast<double>(beam_sum<Tag, VEC>(a.w, BeamRef(ref)));
         d = warp_sum_f64(d);
         const double at = beam_ref(ref);
         if (at != sm.M[w]) d *= exp(at - sm.M[w]);
@@ -851,7 +859,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
             if (has_x) x.mend(P, b, sm);
             if (has_y) y.mend(P, b, sm);
             beam_mend_rows(P, sm);
-            bound -= kMendSlack;
+            bound = beam_slack(bound);
         }
         if (has_x) x.look(sm, bound, take);
         if (has_y) y.look(sm, bound, take);
@@ -864,7 +872,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
                 x.mend(P, b, sm);
             }
             beam_mend_rows(P, sm);
-            bound -= kMendSlack;
+            bound = beam_slack(bound);
         }
         if (few) bound = fmax(bound, beam_visit_bound<Tag, VEC>(P, b, n, sm));
         beam_visit<Tag, VEC>(P, b, n, bound, sm, take);
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(NT, 2) beam_small_kernel(const BeamParams P) {
     auto total = [&](const BeamPlace<Tag, VEC>& p, int u) {
         const float m = from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(fmaxf(p.a.most(), p.xe))));
         const float ref = beam_up(m);
-        double S = beam_far(ref) ? static_cast<double>(beam_sum<Tag, VEC>(p.a.w, ref))
+        double S = beam_far(ref) ? static_cast<double>(beam_sum<Tag, VEC>(p.a.w, BeamRef(ref)))
                                  : beam_sum_exact<Tag, VEC>(p.a.w, p.a.most(), ref, m - kBeamLarge);
         if (p.ie >= 0) S += static_cast<double>(beam_term(p.xe, ref)) + (p.xe >= m - kBeamLarge && !beam_far(ref) ? beam_miss(p.xe, ref) : 0.0);
         S = warp_sum_f64(S);

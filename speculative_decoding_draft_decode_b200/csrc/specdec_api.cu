@@ -232,8 +232,9 @@ BeamLayout make_beam_layout(int B, int W, int V, specdec_dtype dtype) {
     const int64_t all = rows * L.tiles;
     L.seg_tiles = W * L.tiles <= kSmallTiles || all < 1024 ? 1 : all < 4096 ? 2 : 4;
     L.segs = (L.tiles + L.seg_tiles - 1) / L.seg_tiles;
+    // Sized for segments of one tile, so that a smaller call never needs more.
     L.stats = kPartialBase;
-    L.peaks = align_up(L.stats + static_cast<size_t>(rows) * static_cast<size_t>(L.segs) * sizeof(BeamStat), 256);
+    L.peaks = align_up(L.stats + static_cast<size_t>(rows) * static_cast<size_t>(L.tiles) * sizeof(BeamStat), 256);
     L.total = align_up(L.peaks + static_cast<size_t>(rows) * static_cast<size_t>(L.tiles) * sizeof(float), 256);
     return L;
 }

@@ -42,6 +42,11 @@ def test_beam_workspace_size():
     for bad in ((-1, 4, 4, 100, 0), (4, 0, 4, 100, 0), (4, 33, 4, 100, 0), (4, 4, 0, 100, 0), (4, 4, 33, 100, 0),
                 (4, 4, 4, 0, 0), (4, 4, 4, 100, 2)):
         assert f(*bad) == 0, bad
+    # a larger batch, more beams or a longer row never needs less
+    for small, large in (((7, 8, 4, 70000, 1), (8, 8, 4, 70000, 1)), ((3, 10, 4, 128256, 0), (4, 10, 4, 128256, 0)),
+                         ((4, 8, 4, 128000, 1), (4, 9, 4, 128000, 1)), ((63, 4, 4, 16000, 0), (64, 4, 4, 16000, 0)),
+                         ((16, 8, 4, 31000, 1), (16, 8, 4, 33000, 1))):
+        assert f(*small) <= f(*large)
     need = f(4, 4, 4, 1000, 0)
     assert beam(ws_bytes=need - 1) == W
 
