@@ -20,6 +20,7 @@ There is no CPU fallback: if the CUDA library is missing, loading it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -401,12 +402,15 @@ def _current(t, stream):
     return torch.cuda.current_device(), None if stream is None else _stream(stream)
 
 
-def _used_on(stream, *tensors):
-    """Fresh outputs written on another stream than the one they were
-    allocated on: their memory is not handed out again before it is done."""
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        for t in tensors:
-            t.record_stream(stream)
+def _allocating_for(stream):
+    """A context whose fresh tensors belong to the stream the call runs on: a
+    block that another stream has not done with is not handed out for them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def reorder_states(states, parents, lengths=None, time_dim: int = 3, stream=None, out=None):
@@ -453,11 +457,13 @@ def plan_slots(seq_lens, block_tables, held_blocks, free_ring, ring_state, block
         import torch
         B, i32 = seq_lens.numel(), dict(dtype=torch.int32, device=seq_lens.device)
         rows = max(B * (k + 1) if draft_offsets is None else B + total_drafts, 0)
-        out = (torch.empty(B, **i32), torch.empty(B, **i32),
-               ring_state.clone() if B == 0 else torch.empty(2, **i32),
-               torch.empty(rows, dtype=torch.int64, device=seq_lens.device),
-               torch.empty(rows, dtype=torch.int64, device=seq_lens.device))
-        _used_on(stream, *out)
+        with _allocating_for(stream):
+            out = (torch.empty(B, **i32), torch.empty(B, **i32),
+                   ring_state.clone() if B == 0 else torch.empty(2, **i32),
+                   torch.empty(rows, dtype=torch.int64, device=seq_lens.device),
+                   torch.empty(rows, dtype=torch.int64, device=seq_lens.device))
+    elif type(out) is not tuple:
+        out = tuple(out)
     st = _bind().plan_slots(seq_lens, block_tables, held_blocks, free_ring, ring_state, block_size, k, draft_offsets,
                             total_drafts, accept_len, release, out, s, cur)
     if st:
@@ -600,15 +606,18 @@ class Verifier:
         if out is None:
             import torch
             shape, dev = (logits.shape[0], max(num_beams, 0)), logits.device
-            out = (torch.empty(shape, dtype=torch.float32, device=dev), torch.empty(shape, dtype=torch.int32, device=dev),
-                   torch.empty(shape, dtype=torch.int32, device=dev))
-            _used_on(stream, *out)
+            with _allocating_for(stream):
+                out = (torch.empty(shape, dtype=torch.float32, device=dev),
+                       torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.int32, device=dev))
+        elif type(out) is not tuple:
+            out = tuple(out)
         select = _bind().beam_select
         st = select(logits, beam_scores, num_beams, finished, eos_token, out, self._ws, self._ws_bytes, handle, cur)
         if st == SPECDEC_ERR_WORKSPACE:  # the first call, or a larger one than any before
             B, W, V = logits.shape
             need = specdec_workspace_size_beam(B, W, num_beams, V, _dtype_code(logits))
-            ws, wsb = self.workspace(need, stream)
+            with _allocating_for(stream):
+                ws, wsb = self.workspace(need, stream)
             st = select(logits, beam_scores, num_beams, finished, eos_token, out, ws, wsb, handle, cur)
         _check(st, "beam_select")
         return out
