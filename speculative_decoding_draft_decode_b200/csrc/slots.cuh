@@ -14,7 +14,7 @@
 // CTAs, a thread per request (several beyond 8192): the CTAs' totals go
 // through distributed shared memory, so the whole batch is scanned in one
 // launch.  Bound by the latency of its few dependent reads, not by bytes: 64
-// requests of 6 rows 5.2 us, 4096 with 0 to 8 drafts each 10.1 us (two launches).
+// requests of 6 rows 4.7 us, 4096 with 0 to 8 drafts each 9.3 us (two launches).
 // A batch that one CTA holds and whose rows are few gets its positions and
 // slots in the same launch; otherwise plan_slots_kernel writes them.
 #pragma once
@@ -30,6 +30,7 @@
 namespace specdec {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanFew = 256;         // threads for batches of at most so many requests with few rows
 constexpr int kPlanCtas = 8;         // CTAs of the cluster at most (the portable cluster size)
 constexpr int kPlanFusedRows = 8192; // rows that plan_tables_kernel maps itself (one CTA)
 
@@ -157,33 +158,34 @@ __device__ __forceinline__ void plan_move(const PlanParams& P, const PlanMove& m
 // longer moves (prompts, released requests) are shared by its warp.
 constexpr int kPlanTake = 12, kPlanReturn = 4;
 
+template <int THREADS>
 struct PlanSmem {
-    PlanScan warp[kPlanThreads / 32];
+    PlanScan warp[32];
     PlanScan cta[kPlanCtas];        // written by the cluster's CTAs
     unsigned long long taken[kPlanCtas];
     unsigned long long most;
     // one CTA that also maps the rows
-    unsigned len[kPlanThreads];
-    int held[kPlanThreads];         // -1: released
-    int64_t row0[kPlanThreads];
+    unsigned len[THREADS];
+    int held[THREADS];              // -1: released
+    int64_t row0[THREADS];
     uint16_t request[kPlanFusedRows];
 };
 
-template <bool FUSED>
-__global__ void __launch_bounds__(kPlanThreads) plan_tables_kernel(const PlanParams P) {
+template <bool FUSED, int THREADS>
+__global__ void __launch_bounds__(THREADS) plan_tables_kernel(const PlanParams P) {
     namespace cg = cooperative_groups;
-    __shared__ PlanSmem sm;
+    __shared__ PlanSmem<THREADS> sm;
     const int t = threadIdx.x, lane = t & 31, wp = t >> 5;
     const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster
     grid_dependency_wait();
     grid_launch_dependents();
-    const int per = (P.B + ctas * kPlanThreads - 1) / (ctas * kPlanThreads);  // requests of a thread, consecutive
-    const int64_t b0 = (static_cast<int64_t>(rank) * kPlanThreads + t) * per;
+    const int per = (P.B + ctas * THREADS - 1) / (ctas * THREADS);  // requests of a thread, consecutive
+    const int64_t b0 = (static_cast<int64_t>(rank) * THREADS + t) * per;
     const bool backs = P.release != nullptr;
     int64_t head = P.ring_state[0], count = P.ring_state[1];
     const int64_t rows = FUSED ? (P.offsets == nullptr ? static_cast<int64_t>(P.B) * (P.k + 1) : P.B + P.total) : 0;
     if (FUSED && P.offsets != nullptr)
-        for (int i = t; i < rows; i += kPlanThreads) sm.request[i] = 0xffffu;
+        for (int i = t; i < rows; i += THREADS) sm.request[i] = 0xffffu;
     PlanScan mine = {0, 0};
     PlanNeed q = {0, 0, 0, 0, false};
     PlanRows pr = {0, 0};
@@ -201,7 +203,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_tables_kernel(const PlanPar
     PlanScan incl = warp_inclusive(mine, backs);
     if (lane == 31) sm.warp[wp] = incl;
     __syncthreads();
-    PlanScan w = warp_inclusive(sm.warp[lane], backs);  // over the warps, in every warp
+    PlanScan w = {0, 0};
+    if (lane < THREADS / 32) w = sm.warp[lane];
+    w = warp_inclusive(w, backs);  // over the warps, in every warp
     PlanScan all = {__shfl_sync(FULL_MASK, w.grow, 31), __shfl_sync(FULL_MASK, w.back, 31)};
     PlanScan before = {__shfl_sync(FULL_MASK, w.grow, (wp + 31) & 31), __shfl_sync(FULL_MASK, w.back, (wp + 31) & 31)};
     if (wp == 0) before = {0, 0};
@@ -262,28 +266,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_tables_kernel(const PlanPar
             plan_move(P, x, head, count, lane, 32);
         }
     }
-    // The ring after this call: what the last granted request took up to.
+    // The ring after this call.  Everything asked for was there, or what the last
+    // granted request took up to.  (Every CTA read the ring's state before the
+    // cluster's barrier above; the outputs may replace it.)
+    int64_t taken = all.grow;
+    if (all.grow > count) {  // the same in every CTA
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(FULL_MASK, most, o));
-    if (lane == 0 && most > 0) atomicMax(&sm.most, static_cast<unsigned long long>(most));
-    __syncthreads();
-    unsigned long long taken = sm.most;
-    if (!FUSED && ctas > 1) {
-        cg::cluster_group cluster = cg::this_cluster();
-        if (t == 0) cluster.map_shared_rank(&sm, 0)->taken[rank] = taken;
-        cluster.sync();  // also: every CTA has read the ring's state
-        if (rank == 0)
-            for (int i = 0; i < ctas; ++i) taken = max(taken, sm.taken[i]);
+        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(FULL_MASK, most, o));
+        if (lane == 0 && most > 0) atomicMax(&sm.most, static_cast<unsigned long long>(most));
+        __syncthreads();
+        taken = static_cast<int64_t>(sm.most);
+        if (!FUSED && ctas > 1) {
+            cg::cluster_group cluster = cg::this_cluster();
+            if (t == 0) cluster.map_shared_rank(&sm, 0)->taken[rank] = sm.most;
+            cluster.sync();
+            if (rank == 0)
+                for (int i = 0; i < ctas; ++i) taken = max(taken, static_cast<int64_t>(sm.taken[i]));
+        }
     }
+    __syncthreads();
     if (rank == 0 && t == 0) {
         const int64_t back = all.back < P.capacity - count ? all.back : P.capacity - count;
-        int64_t h = head + static_cast<int64_t>(taken);
+        int64_t h = head + taken;
         if (h >= P.capacity) h -= P.capacity;
         P.ring_out[0] = static_cast<int32_t>(h);
-        P.ring_out[1] = static_cast<int32_t>(count - static_cast<int64_t>(taken) + back);
+        P.ring_out[1] = static_cast<int32_t>(count - taken + back);
     }
     if (FUSED) {  // a thread per row; the tables' entries were written by this CTA before the barrier
-        for (int i = t; i < rows; i += kPlanThreads) {
+        for (int i = t; i < rows; i += THREADS) {
             const unsigned b = P.offsets == nullptr ? static_cast<unsigned>(i) / static_cast<unsigned>(P.k + 1) : sm.request[i];
             if (b == 0xffffu) continue;
             const int held = sm.held[b];
