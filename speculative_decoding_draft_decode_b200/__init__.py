@@ -382,10 +382,11 @@ def _bind():
     global _native
     if _native is None:
         lib()  # raises if the library has not been built
+        import torch  # noqa: F401  the binding links against its libraries, which this loads
         try:
             from . import _binding
         except ImportError as e:
-            raise RuntimeError("_binding.so is not built (python -m speculative_decoding_draft_decode_b200.build): %s" % e)
+            raise RuntimeError("_binding.so does not load; build it with python -m speculative_decoding_draft_decode_b200.build: %s" % e)
         _binding.load(library_path)
         _native = _binding
     return _native

@@ -1,5 +1,9 @@
 """Host-side checks of the operators around the verify step: every refusal
 comes before any CUDA call, so these run without a GPU."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -173,3 +177,10 @@ def test_outgrown_workspaces_are_kept(monkeypatch):
     first, n = ver.workspace(1000)
     ver.workspace(5000)
     assert ver._ws is not first and any(w is first for w in ver._outgrown)
+
+
+def test_binding_loads_before_torch_is_imported():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = "import speculative_decoding_draft_decode_b200 as sd; sd._bind()"
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
