@@ -14,7 +14,7 @@
 // CTAs, a thread per request (several beyond 8192): the CTAs' totals go
 // through distributed shared memory, so the whole batch is scanned in one
 // launch.  Bound by the latency of its few dependent reads, not by bytes: 64
-// requests of 6 rows 4.7 us, 4096 with 0 to 8 drafts each 9.3 us (two launches).
+// requests of 6 rows 4.5 us, 4096 with 0 to 8 drafts each 9.6 us (two launches).
 // A batch that one CTA holds and whose rows are few gets its positions and
 // slots in the same launch; otherwise plan_slots_kernel writes them.
 #pragma once
@@ -30,7 +30,7 @@
 namespace specdec {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanFew = 256;         // threads for batches of at most so many requests with few rows
+constexpr int kPlanFew = 256;        // threads for batches of at most so many requests with few rows
 constexpr int kPlanCtas = 8;         // CTAs of the cluster at most (the portable cluster size)
 constexpr int kPlanFusedRows = 8192; // rows that plan_tables_kernel maps itself (one CTA)
 
@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(THREADS) plan_tables_kernel(const PlanParams P
     const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster
     grid_dependency_wait();
     grid_launch_dependents();
+    // Waited for before the first remote write: by then every CTA of the cluster runs.
+    if (!FUSED && ctas > 1) cg::this_cluster().barrier_arrive();
     const int per = (P.B + ctas * THREADS - 1) / (ctas * THREADS);  // requests of a thread, consecutive
     const int64_t b0 = (static_cast<int64_t>(rank) * THREADS + t) * per;
     const bool backs = P.release != nullptr;
@@ -212,6 +214,7 @@ __global__ void __launch_bounds__(THREADS) plan_tables_kernel(const PlanParams P
     PlanScan at = {before.grow + incl.grow - mine.grow, before.back + incl.back - mine.back};
     if (!FUSED && ctas > 1) {
         cg::cluster_group cluster = cg::this_cluster();
+        cluster.barrier_wait();
         if (t < ctas) cluster.map_shared_rank(&sm, t)->cta[rank] = all;
         cluster.sync();
         PlanScan total = {0, 0};
