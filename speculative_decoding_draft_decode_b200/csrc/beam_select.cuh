@@ -187,9 +187,12 @@ __device__ __forceinline__ float beam_end(const typename Tag::storage* row, cons
 
 // Each term is taken as 2^(l c - E) with one rounding in the exponent: c is
 // log2 e in fp32 and E = ref c in fp32, so the terms count from E / c exactly,
-// and c's own error (2^-26 relative) only weighs the distance from there.
-// Values so large that ref c or l c leaves fp32 take l - ref first.
-__device__ __forceinline__ bool beam_far(float ref) { return !(fabsf(ref) < 1e37f); }
+// and c's own error (2^-26 relative) only weighs the distance from there.  The
+// largest logit's term is then 2^(at most E's rounding), which must stay near 1:
+// below 2^16 that is 2^(2^-8), from 2^31 on it could leave fp32.  From 2^16 on a
+// term is 2^((l - ref) c): l - ref is exact for every term that does not vanish
+// (l lies between ref / 2 and 2 ref), so there is one rounding here too.
+__device__ __forceinline__ bool beam_far(float ref) { return !(fabsf(ref) < 65536.0f); }
 __device__ __forceinline__ double beam_ref(float ref) {
     return beam_far(ref) ? static_cast<double>(ref)
                          : static_cast<double>(__fmul_rn(ref, kLog2e)) * (1.0 / static_cast<double>(kLog2e));
@@ -239,8 +242,8 @@ __device__ __noinline__ double beam_miss(float x, float ref) {
 }
 
 // The same sum without its roundings: every term is split on a grid of 2^-20
-// (terms are at most 1 here, so the grid parts add exactly and the rest is below
-// 2^-21), and the lane's largest term (of logit `most`), if it is from `from`
+// (terms are at most 2^(2^-8) here, so the grid parts add exactly up to 16 and the
+// rest is at most 2^-21), and the lane's largest term (of logit `most`), if it is from `from`
 // on, is taken in fp64.  A row's sum errs by its few large terms (the many small
 // ones average out), so the tiles that hold candidates are summed this way.  Not
 // for far references.

@@ -210,6 +210,43 @@ def test_huge_logits(torch_, ver):
     check(torch_, ver, x, beam_scores(rng, 3, 2), 6)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [-1e6, -1e8, -1e9, -2.5e9, -1e10, -1e15, -1e20, -1e30, -1e36])
+def test_masks_of_finite_values(torch_, ver, dtype, low):
+    """Masks of a large finite value: stretches of whole tiles (and of whole
+    segments of them) at the start, in the middle and at the end of a row, whole
+    rows, and scattered tokens; with one launch, with mended sums and without."""
+    rng = np.random.default_rng(23)
+    for W, V in ((2, 3000), (3, 7000), (3, 30000), (2, 41001)):
+        x = logits(rng, 6, W, V)
+        x[0, :, :V // 2] = low
+        x[1, :, V // 4:3 * V // 4] = low
+        x[2, :, V // 3:] = low
+        x[3] = np.where(rng.random((W, V)) < 0.7, low, x[3])
+        x[4, 0] = low                       # nothing else in one row
+        x[5] = low                          # nor in a request
+        x[5, 1, 7:9] = low * 1.5
+        check(torch_, ver, x, beam_scores(rng, 6, W), 6, dtype)
+        check(torch_, ver, x, beam_scores(rng, 6, W), 24, dtype, pad=1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [3e4, 65530.0, 65536.0, 7e4, 9.9e5, 1.1e6, 1e8, 1e9, 2.5e9, 1e10, 1e15, 1e20, 1e30, 1e36, 1.01e37])
+def test_far_references(torch_, ver, dtype, at):
+    """Rows around any finite value, of either sign: close to it, spread around
+    it, of nothing but it, and in stretches of it among ordinary logits."""
+    rng = np.random.default_rng(24)
+    for W, V in ((2, 3000), (3, 7000), (3, 30000)):
+        x = rng.standard_normal((6, W, V)) * 2.0
+        for b, v in enumerate((at, -at)):
+            x[b] = v + x[b]
+            x[2 + b] = v * (1.0 + 1e-2 * x[2 + b])
+        x[4, :, V // 2:] = at
+        x[5, 0] = -at
+        x[5, 1] = at
+        check(torch_, ver, x.astype(np.float32), beam_scores(rng, 6, W), 7, dtype)
+
+
 def test_large_vocabulary(torch_, ver):
     """2^20 + 3 tokens: a row's partials span many chunks."""
     torch = torch_
