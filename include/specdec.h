@@ -439,8 +439,10 @@ specdec_status specdec_ngram_propose(const int32_t* tokens, int64_t token_stride
  * +inf logit in a row that is read, gets scores NaN, parents and tokens -1.
  * The row sums are taken in fp32 per vector and fp64 beyond, values are
  * compared in fp64 and rounded once: scores are within 2^-24 relative plus
- * 4e-6 absolute of the definition, and candidates whose values differ by more
- * than 8e-6 are in the definition's order (candidates of one beam always are).
+ * 4e-6 absolute of the definition.  Candidates of one beam are in the order of
+ * their logits; those of different beams are in the definition's order where
+ * their values differ by more than 8e-6 + 2^-50 of the larger number among
+ * score, logit and value.
  * Limits: 1 <= W, K <= SPECDEC_MAX_BEAMS.  Workspace:
  * specdec_workspace_size_beam; its contents need no initialisation for this
  * call, and the words other calls need zero stay as they are. */

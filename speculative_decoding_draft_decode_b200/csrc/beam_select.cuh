@@ -348,6 +348,7 @@ struct BeamMergeSmem {
     double s[kMaxBeams];
     double add[kMaxBeams];   // s - M - logS
     double S[kMaxBeams];     // sum exp(l - M)
+    float near[kMaxBeams];   // logits nearer to zero may share a value (see beam_near)
     long long fix[kMaxBeams];  // what its roundings are known to have cost, in units of 2^-52
     int state[kMaxBeams];    // 0: no candidates, 1: streamed, 2: finished
     double c[kMergeCand];    // tiles, then candidates
@@ -358,6 +359,7 @@ struct BeamMergeSmem {
     double red_c[NWARPS];
     uint32_t red_id[NWARPS];
     int tiles, cands;
+    int close;               // a logit that may share its value was seen
 };
 
 constexpr double kFixUnit = 4503599627370496.0;  // 2^52: whole numbers add in any order
@@ -374,6 +376,52 @@ __device__ __forceinline__ double beam_value(const BeamMergeSmem& sm, int w, flo
 // Candidates are named (w << 24) + token and tiles (w << 16) + tile: both in
 // the order of w V + token.
 constexpr int kTokenBits = 24, kTileBits = 16;
+
+// Two logits of a row may have one value in 64 bits: logits next to zero, or
+// scores that are large numbers.  They keep the logits' order.  Every step of a
+// value rounds by at most 2^-53 of 2 (|s| + |M| + 64 + |x|) (log S is below 32),
+// while neighbours of x in fp32 lie 2^-24 |x| apart, so it takes an |x| below
+// 2^-22 (|s| + |M| + 64); where none was seen the names alone order equal values.
+__device__ __forceinline__ float beam_near(double s, double M) {
+    return static_cast<float>((fabs(s) + fabs(M) + 64.0) * 0x1p-22);
+}
+
+__device__ __forceinline__ float beam_logit(float x) { return x; }
+__device__ __forceinline__ float beam_logit(uint16_t x) { return bf16_bits_to_float(x); }
+template <class T, int BITS>
+__device__ __noinline__ bool beam_by_logit(const T* logits, int64_t stride, uint32_t id, uint32_t jd) {
+    auto logit = [&](uint32_t i) { return beam_logit(logits[(i >> BITS) * stride + (i & ((1u << BITS) - 1u))]); };
+    const float x = logit(id), y = logit(jd);
+    return x > y || (x == y && id < jd);
+}
+
+// The order of a request's candidates, or of its tiles by their largest logits:
+// name (w << BITS) + i is that of element i of row w.
+template <class T, int BITS>
+struct BeamTies {
+    const T* logits;
+    int64_t stride;
+    bool close;
+    // Whether a value c named id stands before d named jd.
+    __device__ __forceinline__ bool before(double c, uint32_t id, double d, uint32_t jd) const {
+        if (c != d) return c > d;
+        if (close && id != jd && (id >> BITS) == (jd >> BITS)) return beam_by_logit<T, BITS>(logits, stride, id, jd);
+        return id < jd;
+    }
+};
+// The same where no value is shared by different logits.
+struct BeamNoTies {
+    __device__ __forceinline__ bool before(double c, uint32_t id, double d, uint32_t jd) const {
+        return c > d || (c == d && id < jd);
+    }
+};
+template <class Tag>
+__device__ __forceinline__ BeamTies<typename Tag::storage, kTokenBits> beam_ties(const BeamParams& P, int64_t b, bool close) {
+    return {static_cast<const typename Tag::storage*>(P.logits) + b * P.W * P.row_stride, P.row_stride, close};
+}
+__device__ __forceinline__ BeamTies<float, kTileBits> beam_tile_ties(const BeamParams& P, int64_t b, bool close) {
+    return {P.peaks + b * P.W * P.tiles, P.tiles, close};
+}
 
 // A lane's part of a row's n segments: kSegs of them, 32 apart, from i0 on.
 constexpr int kSegs = 4;
@@ -423,22 +471,24 @@ __device__ __forceinline__ BeamStat beam_row_sum(const BeamStat* p, int n, BeamS
     }
 }
 
-// The best (c, id), larger c first and then the lower id, of one per thread.
-// CTA-collective; every thread gets it.
+// The best (c, id), larger c first and then by `ties`, of one per thread (id
+// kBeamNone: none).  CTA-collective; every thread gets it.
 struct BeamBest {
     double c;
     uint32_t id;
 };
+constexpr uint32_t kBeamNone = 0xffffffffu;  // no name: tokens of beam 255
 __device__ __forceinline__ bool beam_before(double c, uint32_t id, double d, uint32_t jd) {
     return c > d || (c == d && id < jd);
 }
-__device__ __forceinline__ BeamBest beam_block_best(BeamBest x, BeamMergeSmem& sm) {
+template <class Ties>
+__device__ __forceinline__ BeamBest beam_block_best(BeamBest x, const Ties& ties, BeamMergeSmem& sm) {
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const double c = __shfl_xor_sync(FULL_MASK, x.c, o);
         const uint32_t id = __shfl_xor_sync(FULL_MASK, x.id, o);
-        if (beam_before(c, id, x.c, x.id)) {
+        if (ties.before(c, id, x.c, x.id)) {
             x.c = c;
             x.id = id;
         }
@@ -449,7 +499,7 @@ __device__ __forceinline__ BeamBest beam_block_best(BeamBest x, BeamMergeSmem& s
     }
     __syncthreads();
     for (int q = 0; q < NWARPS; ++q)
-        if (beam_before(sm.red_c[q], sm.red_id[q], x.c, x.id)) {
+        if (ties.before(sm.red_c[q], sm.red_id[q], x.c, x.id)) {
             x.c = sm.red_c[q];
             x.id = sm.red_id[q];
         }
@@ -465,21 +515,22 @@ __device__ __forceinline__ void beam_output(const BeamParams& P, int64_t at, dou
 
 // The K best tiles of more than kMergeTiles at the bound (runs of equal
 // values): the best one behind the last one found, K times.
-__device__ __noinline__ int beam_many_tiles(const BeamParams& P, const float* peaks, BeamMergeSmem& sm) {
+__device__ __noinline__ int beam_many_tiles(const BeamParams& P, int64_t b, const float* peaks, BeamMergeSmem& sm) {
     const int total = P.W * P.tiles;
+    const auto ties = beam_tile_ties(P, b, sm.close != 0);
     BeamBest last = {INFINITY, 0u};
     for (int i = 0; i < P.K; ++i) {
-        BeamBest best = {-INFINITY, 0xffffffffu};
+        BeamBest best = {-INFINITY, kBeamNone};
         for (int j = threadIdx.x; j < total; j += NT) {
             const int w = j / P.tiles;
             const float m = sm.state[w] == 1 ? __ldcg(&peaks[j]) : -INFINITY;
             if (!(m > -INFINITY)) continue;
             const double c = beam_value(sm, w, m);
             const uint32_t id = (static_cast<uint32_t>(w) << kTileBits) + static_cast<uint32_t>(j - w * P.tiles);
-            if (beam_before(last.c, last.id, c, id) && beam_before(c, id, best.c, best.id)) best = {c, id};
+            if (ties.before(last.c, last.id, c, id) && ties.before(c, id, best.c, best.id)) best = {c, id};
         }
-        last = beam_block_best(best, sm);
-        if (last.id == 0xffffffffu) return i;
+        last = beam_block_best(best, ties, sm);
+        if (last.id == kBeamNone) return i;
         if (threadIdx.x == 0) {
             sm.tile_c[i] = last.c;
             sm.tile_id[i] = last.id;
@@ -536,7 +587,8 @@ struct BeamPlace {
             atomicAdd(reinterpret_cast<unsigned long long*>(&sm.fix[w]),
                       static_cast<unsigned long long>(__double2ll_rn(d * kFixUnit)));
     }
-    // Every element of this lane with a value of at least `bound`: f(c, id).
+    // Every element of this lane with a value of at least `bound`: f(c, id, whether
+    // its value may be another logit's too).
     template <class F>
     __device__ __forceinline__ void look(const BeamMergeSmem& sm, double bound, F f) const {
         const int lane = threadIdx.x & 31;
@@ -548,7 +600,8 @@ struct BeamPlace {
         auto offer = [&](float x, int e) {
             if (x >= low) {
                 const double c = beam_value(sm, w, x);
-                if (c >= bound) f(c, (static_cast<uint32_t>(w) << kTokenBits) + static_cast<uint32_t>(e));
+                if (c >= bound)
+                    f(c, (static_cast<uint32_t>(w) << kTokenBits) + static_cast<uint32_t>(e), fabsf(x) < sm.near[w]);
             }
         };
         if (ie >= 0) offer(xe, ie);
@@ -590,7 +643,7 @@ __device__ __forceinline__ bool beam_ended(const BeamParams& P, const BeamMergeS
 template <class F>
 __device__ __forceinline__ void beam_look_ended(const BeamParams& P, const BeamMergeSmem& sm, double bound, F f) {
     if (beam_ended(P, sm) && sm.s[threadIdx.x] >= bound)
-        f(sm.s[threadIdx.x], (threadIdx.x << kTokenBits) + static_cast<uint32_t>(P.eos));
+        f(sm.s[threadIdx.x], (threadIdx.x << kTokenBits) + static_cast<uint32_t>(P.eos), false);
 }
 
 // Every candidate of the n best tiles and the finished beams with a value of at
@@ -621,13 +674,14 @@ __device__ __noinline__ double beam_visit_bound(const BeamParams& P, int64_t b, 
 // one found, K times.
 template <class Tag, int VEC>
 __device__ __noinline__ void beam_many_candidates(const BeamParams& P, int64_t b, int n, double bound, BeamMergeSmem& sm) {
+    const auto ties = beam_ties<Tag>(P, b, sm.close != 0);
     BeamBest last = {INFINITY, 0u};
     for (int i = 0; i < P.K; ++i) {
-        BeamBest best = {-INFINITY, 0xffffffffu};
-        beam_visit<Tag, VEC>(P, b, n, bound, sm, [&](double c, uint32_t id) {
-            if (beam_before(last.c, last.id, c, id) && beam_before(c, id, best.c, best.id)) best = {c, id};
+        BeamBest best = {-INFINITY, kBeamNone};
+        beam_visit<Tag, VEC>(P, b, n, bound, sm, [&](double c, uint32_t id, bool) {
+            if (ties.before(last.c, last.id, c, id) && ties.before(c, id, best.c, best.id)) best = {c, id};
         });
-        last = beam_block_best(best, sm);
+        last = beam_block_best(best, ties, sm);
         if (threadIdx.x == 0) beam_output(P, b * P.K + i, last.c, last.id);
     }
 }
@@ -666,6 +720,7 @@ __device__ __forceinline__ bool beam_rows(const BeamParams& P, int64_t b, BeamMe
             sm.s[w] = static_cast<double>(s);
             sm.add[w] = (static_cast<double>(s) - M) - logS;
             sm.S[w] = S;
+            sm.near[w] = beam_near(static_cast<double>(s), M);
             sm.fix[w] = 0;
             sm.state[w] = state;
         }
@@ -691,7 +746,17 @@ __device__ __forceinline__ void beam_mend_rows(const BeamParams& P, BeamMergeSme
     __syncthreads();
 }
 
+// How many of n candidates (or tiles) in shared memory stand before one, where
+// values may be shared.
+template <class Ties>
+__device__ __noinline__ int beam_rank_close(const Ties ties, const BeamMergeSmem& sm, int n, double c, uint32_t id) {
+    int rank = 0;
+    for (int i = 0; i < n; ++i) rank += ties.before(sm.c[i], sm.id[i], c, id) ? 1 : 0;
+    return rank;
+}
+
 // The outputs from at most kMergeCand candidates in shared memory.
+template <class Tag>
 __device__ __forceinline__ void beam_rank(const BeamParams& P, int64_t b, BeamMergeSmem& sm, int cands) {
     const int t = threadIdx.x, K = P.K;
     // A candidate's rank is its place.  Among many, those below the bound of
@@ -733,6 +798,7 @@ __device__ __forceinline__ void beam_rank(const BeamParams& P, int64_t b, BeamMe
         int rank = 0;
 #pragma unroll 4
         for (int i = 0; i < ranked; ++i) rank += beam_before(sm.c[i], sm.id[i], own_c[j], own_id[j]) ? 1 : 0;
+        if (sm.close != 0) rank = beam_rank_close(beam_ties<Tag>(P, b, true), sm, ranked, own_c[j], own_id[j]);
         if (rank < K) beam_output(P, b * K + rank, own_c[j], own_id[j]);
     }
     for (int i = cands + t; i < K; i += NT) {
@@ -761,7 +827,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         const int i = nth(j);
         m[j] = j * NT < total && i < total ? __ldcg(&peaks[i]) : -INFINITY;
     }
-    if (t == 0) sm.tiles = sm.cands = 0;
+    if (t == 0) sm.tiles = sm.cands = sm.close = 0;
     if (beam_rows(P, b, sm, [&](int w) {
             const BeamStat* p = P.stats + (b * P.W + w) * P.segs;
             if (w != wp) first.load(p, 0, P.segs);
@@ -793,11 +859,11 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         if (i < total) best = fmax(best, value(i, __ldcg(&peaks[i])));
     }
     const double floor = beam_bound(best, K, sm);
-    auto keep = [&](double v, int i) {
+    auto keep = [&](double v, int i, float x) {
         if (!(v >= floor && v > -INFINITY)) return;
-        const int at = atomicAdd(&sm.tiles, 1);
+        const int at = atomicAdd(&sm.tiles, 1), w = row_of(i);
+        if (fabsf(x) < sm.near[w]) sm.close = 1;
         if (at < kMergeTiles) {
-            const int w = row_of(i);
             sm.c[at] = v;
             const uint32_t id = (static_cast<uint32_t>(w) << kTileBits) + static_cast<uint32_t>(i - w * P.tiles);
             sm.id[at] = id;
@@ -806,10 +872,11 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
     };
 #pragma unroll
     for (int j = 0; j < kMergePeaks; ++j)
-        if (j * NT < total) keep(c[j], nth(j));
+        if (j * NT < total) keep(c[j], nth(j), m[j]);
     for (int j = kMergePeaks; j * NT < total; ++j) {
         const int i = nth(j);
-        if (i < total) keep(value(i, __ldcg(&peaks[i])), i);
+        const float x = i < total ? __ldcg(&peaks[i]) : -INFINITY;
+        if (i < total) keep(value(i, x), i, x);
     }
     __syncthreads();
     // Few enough tiles to hold in registers are all taken; of more the K best, a
@@ -826,18 +893,20 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
                 int rank = 0;
 #pragma unroll 4
                 for (int j = 0; j < have; ++j) rank += beam_before(sm.c[j], sm.id[j], v, id) ? 1 : 0;
+                if (sm.close != 0) rank = beam_rank_close(beam_tile_ties(P, b, true), sm, have, v, id);
                 if (rank < K) {
                     sm.tile_c[rank] = v;
                     sm.tile_id[rank] = id;
                 }
             }
         } else {
-            n = beam_many_tiles(P, peaks, sm);
+            n = beam_many_tiles(P, b, peaks, sm);
         }
         __syncthreads();
         bound = n == K ? sm.tile_c[K - 1] : -INFINITY;
     }
-    auto take = [&](double v, uint32_t id) {
+    auto take = [&](double v, uint32_t id, bool close) {
+        if (close) sm.close = 1;
         const int at = atomicAdd(&sm.cands, 1);
         if (at < kMergeCand) {
             sm.c[at] = v;
@@ -891,7 +960,7 @@ __device__ __forceinline__ void beam_merge(const BeamParams& P, int64_t b, BeamM
         cands = sm.cands;
     }
     if (cands > kMergeCand) beam_many_candidates<Tag, VEC>(P, b, n, bound, sm);
-    else beam_rank(P, b, sm, cands);
+    else beam_rank<Tag>(P, b, sm, cands);
 }
 
 // Rows of many tiles: a warp per segment, then a CTA per request.  The second
@@ -934,7 +1003,7 @@ __global__ void __launch_bounds__(NT, 2) beam_small_kernel(const BeamParams P) {
     grid_launch_dependents();
     const int64_t b = blockIdx.x;
     const int units = P.W * P.tiles;  // unit u: tile u % tiles of beam u / tiles
-    if (t == 0) sm.cands = 0;
+    if (t == 0) sm.cands = sm.close = 0;
     if (t < kSmallTiles) sm.tile_id[t] = static_cast<uint32_t>(t / P.tiles << kTileBits) + static_cast<uint32_t>(t % P.tiles);
     __syncthreads();
     BeamPlace<Tag, VEC> x, y;
@@ -979,7 +1048,8 @@ __global__ void __launch_bounds__(NT, 2) beam_small_kernel(const BeamParams P) {
     if (has_x) e = fmax(e, x.best(sm));
     if (has_y) e = fmax(e, y.best(sm));
     const double bound = beam_bound(e, P.K, sm);
-    auto take = [&](double v, uint32_t id) {
+    auto take = [&](double v, uint32_t id, bool close) {
+        if (close) sm.close = 1;
         const int at = atomicAdd(&sm.cands, 1);
         if (at < kMergeCand) {
             sm.c[at] = v;
@@ -992,22 +1062,28 @@ __global__ void __launch_bounds__(NT, 2) beam_small_kernel(const BeamParams P) {
     __syncthreads();
     const int cands = sm.cands;
     if (cands <= kMergeCand) {
-        beam_rank(P, b, sm, cands);
+        beam_rank<Tag>(P, b, sm, cands);
         return;
     }
     // Runs of equal values: the best one behind the last one found, K times.
-    BeamBest last = {INFINITY, 0u};
-    for (int i = 0; i < P.K; ++i) {
-        BeamBest best = {-INFINITY, 0xffffffffu};
-        auto offer = [&](double c, uint32_t id) {
-            if (beam_before(last.c, last.id, c, id) && beam_before(c, id, best.c, best.id)) best = {c, id};
-        };
-        if (has_x) x.look(sm, bound, offer);
-        if (has_y) y.look(sm, bound, offer);
-        beam_look_ended(P, sm, bound, offer);
-        last = beam_block_best(best, sm);
-        if (t == 0) beam_output(P, b * P.K + i, last.c, last.id);
-    }
+    auto one_by_one = [&](const auto& ties) {
+        BeamBest last = {INFINITY, 0u};
+        for (int i = 0; i < P.K; ++i) {
+            BeamBest best = {-INFINITY, kBeamNone};
+            auto offer = [&](double c, uint32_t id, bool) {
+                if (ties.before(last.c, last.id, c, id) && ties.before(c, id, best.c, best.id)) best = {c, id};
+            };
+            if (has_x) x.look(sm, bound, offer);
+            if (has_y) y.look(sm, bound, offer);
+            beam_look_ended(P, sm, bound, offer);
+            last = beam_block_best(best, ties, sm);
+            if (t == 0) beam_output(P, b * P.K + i, last.c, last.id);
+        }
+    };
+    // 8 x 4 rows of 1000 bf16, K = 32 (all candidates are looked at K times): 143 us,
+    // 201 us in one loop that may compare logits.
+    if (sm.close == 0) one_by_one(BeamNoTies());
+    else one_by_one(beam_ties<Tag>(P, b, true));
 }
 
 }  // namespace specdec

@@ -145,6 +145,33 @@ def test_equal_values(torch_, ver, dtype, K):
     assert (p[0][:min(K, 8)] == np.arange(min(K, 8))).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("W,V", [(2, 700), (2, 9000), (3, 40003)])
+def test_logits_that_differ_less_than_their_values(torch_, ver, dtype, W, V):
+    """Two logits of a row whose values are one number in 64 bits (logits next
+    to zero, or scores so low that no logit shows beside them) are still in the
+    logits' order."""
+    torch = torch_
+    rng = np.random.default_rng(29)
+    x = rng.standard_normal((5, W, V)).astype(np.float32)
+    x[0] *= 1e-18
+    x[1] *= 1e-30
+    x[2, :, V // 2:] *= 1e-20
+    x[2, :, :V // 2] = -1.0
+    x[0, :, 5], x[0, :, 3] = 0.0, -0.0
+    s = np.full((5, W), -1.0, np.float32) - np.arange(W, dtype=np.float32) * 0.125
+    s[3] = -1e30
+    s[4] = np.finfo(np.float32).min
+    t, stored = rows_of(torch, x, dtype)
+    for K in (1, 6, 20, 32):
+        _, p, tok = (host(a) for a in ver.beam_select(t, torch.from_numpy(s).cuda(), K))
+        for b in range(5):
+            assert (p[b] >= 0).all() and len(set(zip(p[b].tolist(), tok[b].tolist()))) == K
+            for w in set(p[b].tolist()):
+                mine = tok[b][p[b] == w]
+                assert np.array_equal(mine, np.argsort(-stored[b, w], kind="stable")[:len(mine)])
+
+
 def test_ties_over_many_chunks(torch_, ver):
     """32 beams of one value over several chunks: more candidates at the bound
     than the merge holds."""
