@@ -433,7 +433,8 @@ specdec_status specdec_ngram_propose(const int32_t* tokens, int64_t token_stride
  *                checked when finished is given.
  *   out_scores   [B, K] float32, descending; out_parents, out_tokens [B, K]
  *                int32: the beam w and the token v of each.  With K == W
- *                out_scores may be beam_scores
+ *                out_scores may be beam_scores; no output may share memory
+ *                with another one or with any other argument
  * A logit of -inf is no candidate; with fewer than K candidates the rest is
  * (-inf, -1, -1).  A request with a score of NaN or +inf, or with a NaN or
  * +inf logit in a row that is read, gets scores NaN, parents and tokens -1.
@@ -493,7 +494,8 @@ specdec_status specdec_reorder_states(const void* src, void* dst, const int32_t*
  *                (held and free).  Pages are taken from the head in request
  *                order and returned behind the tail in request order.
  *   seq_lens_out, held_out, ring_state_out: the new values; each may be the
- *                array it replaces
+ *                array it replaces.  Nothing else that is written may share
+ *                memory with another argument
  *   positions, slots [rows] int64: len_b + j and its slot
  * A request gets all the pages it asks for when the requests up to and
  * including it ask for no more than the ring holds (pages returned in this

@@ -215,6 +215,30 @@ void fill_common(Pass1Params& P, const void* logits, int64_t row_stride, int V, 
 namespace specdec {
 namespace {
 
+// Memory of an argument; none if its address is null.
+struct Span {
+    const void* at;
+    int64_t bytes;
+};
+bool meet(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x != 0 && y != 0 && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) &&
+           y < x + static_cast<uintptr_t>(a.bytes);
+}
+// Whether an output meets another one or an input.  Output i may be input
+// replaces[i] itself (-1: none).
+template <int O, int I>
+bool outputs_meet(const Span (&out)[O], const int (&replaces)[O], const Span (&in)[I]) {
+    for (int i = 0; i < O; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return true;
+        for (int j = 0; j < I; ++j)
+            if (meet(out[i], in[j]) && !(replaces[i] == j && out[i].at == in[j].at && out[i].bytes == in[j].bytes))
+                return true;
+    }
+    return false;
+}
+
 // Beam selection: the segments' sums and the tiles' largest logits, behind the
 // fixed area (which it does not touch).
 struct BeamLayout {
@@ -1064,6 +1088,14 @@ specdec_status specdec_beam_select(const void* logits, specdec_dtype dtype, int6
     const BeamLayout L = make_beam_layout(B, W, V, dtype);
     specdec_status st = check_ws(ws, ws_bytes, L.total);
     if (st != SPECDEC_OK) return st;
+    // A request's outputs are written while other requests' inputs may not have been read.
+    const int64_t got = static_cast<int64_t>(B) * K * 4;
+    const Span out[3] = {{out_scores, got}, {out_parents, got}, {out_tokens, got}};
+    const Span in[4] = {{beam_scores, rows * 4},
+                        {finished, rows * 4},
+                        {logits, ((rows - 1) * row_stride + V) * static_cast<int64_t>(elem_size(dtype))},
+                        {ws, static_cast<int64_t>(L.total)}};
+    if (outputs_meet(out, {0, -1, -1}, in)) return SPECDEC_ERR_INVALID_ARG;
     BeamParams P;
     P.logits = logits;
     P.row_stride = row_stride;
@@ -1216,6 +1248,18 @@ specdec_status specdec_plan_slots(const int32_t* seq_lens, const int32_t* accept
         ring_state == nullptr || seq_lens_out == nullptr || held_out == nullptr || ring_state_out == nullptr ||
         positions == nullptr || slots == nullptr)
         return SPECDEC_ERR_INVALID_ARG;
+    const int64_t rows = draft_offsets != nullptr ? B + total_drafts : static_cast<int64_t>(B) * (k + 1);
+    const int64_t each = static_cast<int64_t>(B) * 4;
+    const Span out[7] = {{seq_lens_out, each},
+                         {held_out, each},
+                         {ring_state_out, 8},
+                         {positions, rows * 8},
+                         {slots, rows * 8},
+                         {block_tables, ((B - 1) * table_stride + max_blocks) * 4},
+                         {free_ring, static_cast<int64_t>(ring_capacity) * 4}};
+    const Span in[6] = {{seq_lens, each}, {held_blocks, each}, {ring_state, 8}, {accept_len, each}, {release, each},
+                        {draft_offsets, each + 4}};
+    if (outputs_meet(out, {0, 1, 2, -1, -1, -1, -1}, in)) return SPECDEC_ERR_INVALID_ARG;
     PlanParams P;
     P.seq_lens = seq_lens;
     P.accept_len = accept_len;
@@ -1238,7 +1282,6 @@ specdec_status specdec_plan_slots(const int32_t* seq_lens, const int32_t* accept
     P.positions = positions;
     P.slots = slots;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t rows = draft_offsets != nullptr ? B + total_drafts : static_cast<int64_t>(B) * (k + 1);
     if (B <= kPlanThreads && rows <= kPlanFusedRows) {
         // 64 requests of 6 rows: 4.7 us with 256 threads, 5.2 us with 1024; 141 of 20
         // rows: 8.7 and 6.4 us.

@@ -112,6 +112,34 @@ def test_plan_refusals():
     assert plan(B=0, seq_lens=None) == OK
 
 
+def apart(*names):
+    return {n: FAKE + (i << 32) for i, n in enumerate(names)}
+
+
+def test_beam_outputs_that_share_memory():
+    """An output over another one, or over an input that other requests still
+    read; only the scores may take the old ones' place, as many as they are."""
+    a = dict(apart("logits", "beam_scores", "out_scores", "out_parents", "out_tokens", "ws", "finished"), K=8)
+    for bad in (dict(out_scores=a["beam_scores"]), dict(out_parents=a["out_scores"]), dict(out_tokens=a["out_parents"] + 124),
+                dict(out_scores=a["beam_scores"] + 60), dict(out_scores=a["beam_scores"] + 4, K=4),
+                dict(out_tokens=a["finished"]), dict(out_parents=a["beam_scores"], K=4),
+                dict(out_scores=a["logits"] + 15 * 4000 + 3996), dict(out_parents=a["ws"] + 1024),
+                dict(out_parents=a["finished"], K=4)):
+        assert beam(**{**a, **bad}) == E, bad
+
+
+def test_plan_outputs_that_share_memory():
+    a = apart("seq_lens", "accept_len", "release", "draft_offsets", "block_tables", "held_blocks", "free_ring",
+              "ring_state", "seq_lens_out", "held_out", "ring_state_out", "positions", "slots")
+    a["total_drafts"] = 16
+    for bad in (dict(seq_lens_out=a["held_out"]), dict(seq_lens_out=a["held_blocks"]), dict(held_out=a["seq_lens"]),
+                dict(held_out=a["held_blocks"] + 4), dict(ring_state_out=a["ring_state"] + 4),
+                dict(ring_state_out=a["free_ring"] + 396), dict(positions=a["slots"]), dict(slots=a["positions"] + 152),
+                dict(slots=a["draft_offsets"] + 16), dict(positions=a["accept_len"]), dict(seq_lens_out=a["release"]),
+                dict(block_tables=a["free_ring"]), dict(block_tables=a["seq_lens"] - 124), dict(free_ring=a["held_blocks"])):
+        assert plan(**{**a, **bad}) == E, bad
+
+
 def test_host_tensors_are_refused():
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     ver = sd.Verifier(torch.device("cuda", 0))
