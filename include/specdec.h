@@ -500,7 +500,8 @@ specdec_status specdec_reorder_states(const void* src, void* dst, const int32_t*
  * A request gets all the pages it asks for when the requests up to and
  * including it ask for no more than the ring holds (pages returned in this
  * call are not granted in it) and its table has room; otherwise none.  A row
- * without a page gets slot -1 (its position is still written). */
+ * without a page gets slot -1 (its position is still written).  With B == 0
+ * only the ring's state is copied. */
 specdec_status specdec_plan_slots(const int32_t* seq_lens, const int32_t* accept_len, const int32_t* release,
                                   const int32_t* draft_offsets, int B, int k, int64_t total_drafts, int block_size,
                                   int32_t* block_tables, int64_t table_stride, int max_blocks,

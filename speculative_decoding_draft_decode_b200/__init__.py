@@ -460,7 +460,7 @@ def plan_slots(seq_lens, block_tables, held_blocks, free_ring, ring_state, block
         rows = max(B * (k + 1) if draft_offsets is None else B + total_drafts, 0)
         with _allocating_for(stream):
             out = (torch.empty(B, **i32), torch.empty(B, **i32),
-                   ring_state.clone() if B == 0 else torch.empty(2, **i32),
+                   torch.empty(2, **i32),
                    torch.empty(rows, dtype=torch.int64, device=seq_lens.device),
                    torch.empty(rows, dtype=torch.int64, device=seq_lens.device))
     elif type(out) is not tuple:

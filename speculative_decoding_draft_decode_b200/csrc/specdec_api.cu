@@ -1243,7 +1243,14 @@ specdec_status specdec_plan_slots(const int32_t* seq_lens, const int32_t* accept
         return SPECDEC_ERR_INVALID_ARG;
     if (draft_offsets != nullptr && (total_drafts < 0 || total_drafts > static_cast<int64_t>(B) * k))
         return SPECDEC_ERR_INVALID_ARG;
-    if (B == 0) return SPECDEC_OK;
+    if (B == 0) {  // nobody takes or returns a page: the ring stays as it is
+        if (ring_state == nullptr || ring_state_out == nullptr || ring_state == ring_state_out) return SPECDEC_OK;
+        if (meet({ring_state, 8}, {ring_state_out, 8})) return SPECDEC_ERR_INVALID_ARG;
+        return cudaMemcpyAsync(ring_state_out, ring_state, 8, cudaMemcpyDeviceToDevice,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? SPECDEC_OK
+                   : SPECDEC_ERR_CUDA;
+    }
     if (seq_lens == nullptr || block_tables == nullptr || held_blocks == nullptr || free_ring == nullptr ||
         ring_state == nullptr || seq_lens_out == nullptr || held_out == nullptr || ring_state_out == nullptr ||
         positions == nullptr || slots == nullptr)

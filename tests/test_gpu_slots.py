@@ -157,6 +157,20 @@ def test_fresh_outputs_and_refusals(torch_, sd_):
             sd_.plan_slots(**{**a, **bad})
 
 
+def test_no_requests(torch_, sd_):
+    """An empty batch leaves the ring as it was, in the outputs given too."""
+    torch = torch_
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    pos, slots = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    state = torch.tensor([3, 7], device="cuda", dtype=torch.int32)
+    a = (i(0), i(0, 4), i(0), i(10), state, 16)
+    for kw in (dict(k=3), dict(k=3, draft_offsets=i(1))):
+        out = (i(0), i(0), torch.full((2,), -9, device="cuda", dtype=torch.int32), pos, slots)
+        assert sd_.plan_slots(*a, out=out, **kw)[2].tolist() == [3, 7]
+        assert sd_.plan_slots(*a, **kw)[2].tolist() == [3, 7]
+        assert sd_.plan_slots(*a, out=(i(0), i(0), state, pos, slots), **kw)[2].tolist() == [3, 7]
+
+
 def test_uneven_rows(torch_, sd_):
     """Packed drafts that stand close together: one CTA's requests have most of
     the rows, more than it maps at a time."""
