@@ -10,11 +10,14 @@ PyTorch build.  No fast-math: the rejection statistics rely on IEEE expf.
 
 The torch binding of the calls around the verify step (_binding.so, from
 csrc/binding.cpp): host code only, against the headers of the PyTorch that is
-installed.
+installed, and built again when that is another one.  Without PyTorch only the
+library is built, which C programs use alone.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -48,8 +51,26 @@ def _newer(target, srcs) -> bool:
     return all(os.path.getmtime(s) <= t for s in srcs)
 
 
+def _built_for() -> str:
+    """What a binding is good for; it carries this text."""
+    try:
+        version = importlib.metadata.version("torch")  # without the time its import takes
+    except importlib.metadata.PackageNotFoundError:
+        from torch import __version__ as version
+    return "torch %s, %s" % (version, sysconfig.get_config_var("SOABI"))
+
+
+def _binding_up_to_date() -> bool:
+    if importlib.util.find_spec("torch") is None:
+        return True  # none can be built
+    if not _newer(BINDING, [BINDING_MAIN, HEADER]):
+        return False
+    with open(BINDING, "rb") as f:
+        return _built_for().encode() + b"\0" in f.read()
+
+
 def up_to_date() -> bool:
-    return _newer(LIB, sources()) and _newer(BINDING, [BINDING_MAIN, HEADER])
+    return _newer(LIB, sources()) and _binding_up_to_date()
 
 
 def _build_library(verbose: bool) -> None:
@@ -69,7 +90,7 @@ def _build_binding(verbose: bool) -> None:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     tmp = BINDING + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), '-DBUILT_FOR="%s"' % _built_for(),
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
            BINDING_MAIN, "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
@@ -83,7 +104,9 @@ def _build_binding(verbose: bool) -> None:
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or not _newer(LIB, sources()):
         _build_library(verbose)
-    if force or not _newer(BINDING, [BINDING_MAIN, HEADER]):
+    if importlib.util.find_spec("torch") is None:
+        print("PyTorch is not installed: its binding (_binding.so) is not built", file=sys.stderr)
+    elif force or not _binding_up_to_date():
         _build_binding(verbose)
     return LIB
 

@@ -212,3 +212,18 @@ def test_binding_loads_before_torch_is_imported():
     code = "import speculative_decoding_draft_decode_b200 as sd; sd._bind()"
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_the_library_is_built_without_torch(monkeypatch, tmp_path, capsys):
+    """C programs use the library alone: a machine without PyTorch builds it."""
+    monkeypatch.setattr(sd_build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert sd_build.build() == sd_build.LIB
+    assert not (tmp_path / "_binding.so").exists() and "not built" in capsys.readouterr().err
+
+
+def test_a_binding_of_another_torch_is_stale(monkeypatch):
+    import importlib.metadata
+    assert sd_build.up_to_date()
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0.1")
+    assert not sd_build.up_to_date()
