@@ -15,11 +15,12 @@
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <cstdarg>
-#include <cstdio>
+#include <algorithm>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "../../include/specdec.h"
 
@@ -102,6 +103,21 @@ int64_t row_elems(const at::Tensor& t, int64_t lead, const char* name) {
         n *= t.size(d);
     }
     return n;
+}
+
+// Rows that are written (`row` elements each, over the first `lead` dimensions)
+// must not share memory: from the smallest stride on, each has to pass what lies
+// within it.
+void rows_apart(const at::Tensor& t, int64_t lead, int64_t row) {
+    std::vector<std::pair<int64_t, int64_t>> d;  // stride, size
+    for (int64_t i = 0; i < lead; ++i)
+        if (t.size(i) > 1) d.emplace_back(t.stride(i), t.size(i));
+    std::sort(d.begin(), d.end());
+    int64_t extent = row;
+    for (const auto& [stride, size] : d) {
+        if (stride < extent) throw Refused("the rows written must not share memory");
+        extent += stride * (size - 1);
+    }
 }
 
 template <class F>
@@ -195,8 +211,8 @@ PyObject* reorder_states(PyObject*, PyObject* const* a, Py_ssize_t n) {
             const int d = i < 3 ? i : i == 3 ? (td == 4 ? 3 : -1) : td;
             ss[i] = d < 0 ? 0 : x.stride(d) * es;
             ds[i] = d < 0 ? 0 : to.stride(d) * es;
-            if (d >= 0 && to.size(d) > 1 && to.stride(d) < row) throw Refused("the rows written must not share memory");
         }
+        rows_apart(to, td + 1, row);
         if (B > INT_MAX || W > INT_MAX) return SPECDEC_ERR_INVALID_ARG;
         return f_reorder_states(x.data_ptr(), to.data_ptr(), static_cast<const int32_t*>(parents),
                                 static_cast<const int32_t*>(lengths), G, static_cast<int>(B), static_cast<int>(W), H, T,
@@ -249,7 +265,7 @@ PyObject* commit_path(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool same = paged && src.data_ptr() == dst.data_ptr() && src.strides() == dst.strides();
         if (!same && overlap(src, dst))
             throw Refused("src and dst overlap: in place both must be the same cache, with src_slots");
-        if (dst.size(0) > 1 && dst.stride(0) < row) throw Refused("the rows written must not share memory");
+        rows_apart(dst, 2, row);
         const int64_t es = static_cast<int64_t>(src.element_size());
         const int64_t rows = paged ? src.size(1) : src.size(2);  // rows along the row stride
         int64_t sr = paged ? src.stride(1) : src.stride(2), dr = dst.stride(1);

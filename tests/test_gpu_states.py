@@ -289,6 +289,29 @@ def test_commit_refusals(torch_, sd_):
         sd_.commit_path(src, i(3), i(3, 33), dst, torch.zeros(3, 34, dtype=torch.int64, device="cuda"))
 
 
+def test_rows_that_share_memory(torch_, sd_):
+    """Windows of one buffer: a row written is a part of another one."""
+    torch = torch_
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    flat = torch.zeros(4096, device="cuda")
+    for shape, strides in (((1, 2, 3, 4, 8), (0, 96, 8, 8, 1)), ((2, 2, 3, 4, 8), (64, 96, 32, 8, 1)),
+                           ((1, 2, 3, 4, 8), (0, 88, 32, 8, 1))):
+        x = flat.as_strided(shape, strides)
+        with pytest.raises(ValueError, match="share memory"):
+            sd_.reorder_states(x, i(*shape[1:3]))
+        with pytest.raises(ValueError, match="share memory"):
+            sd_.reorder_states(torch.zeros(shape, device="cuda"), i(*shape[1:3]), out=x)
+    sl = torch.zeros(3, 5, dtype=torch.int64, device="cuda")
+    for strides in ((8, 8, 1), (16, 12, 1), (72, 8, 1)):
+        with pytest.raises(ValueError, match="share memory"):
+            sd_.commit_path(torch.zeros(2, 3, 5, 8, device="cuda"), i(3), i(3, 4), flat.as_strided((2, 10, 8), strides), sl)
+    # groups within positions, and gaps anywhere, are no such case
+    for t in (flat[:2 * 10 * 8].view(10, 2, 8).transpose(0, 1), flat.as_strided((2, 10, 8), (11, 30, 1))):
+        sd_.commit_path(torch.zeros(2, 3, 5, 8, device="cuda"), i(3) - 1, i(3, 4), t, sl)
+    x = torch.zeros(4, 3, 2, 5, 8, device="cuda").permute(2, 1, 3, 0, 4)
+    assert sd_.reorder_states(x, i(3, 5)) is x
+
+
 def test_other_current_device_is_refused(torch_, sd_, monkeypatch):
     """Tensors of another device than the current one: refused, nothing launched."""
     torch = torch_
