@@ -1007,12 +1007,13 @@ __global__ void __launch_bounds__(NT, 2) beam_small_kernel(const BeamParams P) {
     if (t < kSmallTiles) sm.tile_id[t] = static_cast<uint32_t>(t / P.tiles << kTileBits) + static_cast<uint32_t>(t % P.tiles);
     __syncthreads();
     BeamPlace<Tag, VEC> x, y;
-    bool has_x = wp < units, has_y = wp + NWARPS < units;
-    // Loaded before it is known whether the rows are streamed.
+    // Rows that are not streamed are not read.
+    auto streams = [&](int u) {
+        return u < units && beam_streams(P, b * P.W + static_cast<int>(sm.tile_id[u] >> kTileBits));
+    };
+    bool has_x = streams(wp), has_y = streams(wp + NWARPS);
     if (has_x) x.load(P, b, sm, wp);
     if (has_y) y.load(P, b, sm, wp + NWARPS);
-    has_x = has_x && beam_streams(P, b * P.W + x.w);
-    has_y = has_y && beam_streams(P, b * P.W + y.w);
     auto total = [&](const BeamPlace<Tag, VEC>& p, int u) {
         const float m = from_ord_i32(__reduce_max_sync(FULL_MASK, ord_i32(fmaxf(p.a.most(), p.xe))));
         const float ref = beam_up(m);
