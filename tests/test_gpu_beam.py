@@ -146,7 +146,7 @@ def test_equal_values(torch_, ver, dtype, K):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("W,V", [(2, 700), (2, 9000), (3, 40003)])
+@pytest.mark.parametrize("W,V", [(2, 700), (2, 9000), (3, 40003), (3, 400003)])
 def test_logits_that_differ_less_than_their_values(torch_, ver, dtype, W, V):
     """Two logits of a row whose values are one number in 64 bits (logits next
     to zero, or scores so low that no logit shows beside them) are still in the
