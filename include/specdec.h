@@ -575,7 +575,8 @@ const char* specdec_status_string(specdec_status status);
  * while letting its dependents start early (a kernel that executes
  * griddepcontrol.launch_dependents before its last store of the logits);
  * kernels without programmatic launch, memory copies, and this library's
- * own kernels are safe.  The setting is read when a call is enqueued (and
+ * own kernels are safe, except for a specdec_reorder_states or
+ * specdec_commit_path call that moves those very logits.  The setting is read when a call is enqueued (and
  * baked into a captured graph). */
 int specdec_set_prefetch_inputs(int enable);
 

@@ -6,8 +6,9 @@
 // every beam): it loads each parent that moves once and then stores to all of
 // its children, so the move is safe in place and a parent is read once
 // however many children it has.  16 groups of 8 x 8 beams of up to 1024 x 512
-// bf16: 167 us for 1.11 GB, 6.6 TB/s; in place, heads before positions, 15 us
-// for 84 MB, 5.5 TB/s.
+// bf16 (random lengths, mean of three inputs): 168 us for 1.09 GB read and
+// written, 6.5 TB/s, as fast as a plain copy; 6 groups and 7 heads of 5 x 5 beams
+// of up to 333 x 80 fp32 in place, 14.4 us for 53 MB, 3.7 TB/s.
 //
 // commit_path_kernel: draft trees (handbook page, "Medusa": the longest
 // accepted candidate prefix is kept).  The states of the root and of the
@@ -15,7 +16,7 @@
 // depth j has an index >= j, so in place (source and destination rows of one
 // cache, addressed by the same slots) row j is written only after every row
 // with an index <= j has been read.  A few dependent reads, then a copy: 8
-// groups of 256 requests with 1000-byte rows 5.0 us for 20 MB, 4.1 TB/s.
+// groups of 256 requests with 1000-byte rows 5.3 us for 20 MB, 3.9 TB/s.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -114,7 +115,8 @@ __global__ void __launch_bounds__(NT) reorder_states_kernel(const ReorderParams 
 // of every row of dst and puts each together from the two aligned 16-byte words
 // of src that hold them (both hold a byte of the run, so no other memory is
 // touched; the neighbouring threads' words come from L1).  28 groups of 9 beams
-// of 472 x 249 bf16: 21.9 us for 61 MB, 33.9 us in 2-byte accesses.
+// of 472 x 249 bf16: 21.9 us for 61 MB (2.8 TB/s; two loads for every store, and
+// a parent's words once for each of its children), 33.9 us in 2-byte accesses.
 __device__ __forceinline__ uint4 shift_words(const uint4& a, const uint4& b, int bytes) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t x[5];
