@@ -3,7 +3,7 @@
 The verifier's CUDA library:
 
     nvcc -O3 -std=c++17 -gencode arch=compute_100a,code=sm_100a -lineinfo
-         -Xcompiler -fPIC -shared csrc/specdec_api.cu -o libspecdec.so
+         -Xcompiler -fPIC -shared csrc/libspecdec.cu -o libspecdec.so
 
 The CUDA runtime is linked statically, so the library loads next to any
 PyTorch build.  No fast-math: the rejection statistics rely on IEEE expf.
@@ -27,7 +27,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libspecdec.so")
 BINDING = os.path.join(HERE, "_binding.so")
-MAIN = os.path.join(HERE, "csrc", "specdec_api.cu")
+MAIN = os.path.join(HERE, "csrc", "libspecdec.cu")
 BINDING_MAIN = os.path.join(HERE, "csrc", "binding.cpp")
 HEADER = os.path.join(ROOT, "include", "specdec.h")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -146,3 +146,13 @@ def test_rows_of_each_layout():
     off = np.array([0, 1, 4, 4, 11], np.int32)
     rg = gen.RaggedInputs("shape", gen.BF16, None, None, off, 4, 7, 100)
     assert bench.rows_of(rg) == 15 and bench.rows_of(rg, 2) == 4 + 2
+
+
+def test_the_traffic_record_is_the_verifiers():
+    """The recorded memory traffic holds until the verifier's own sources change:
+    the calls around the verify step are not among them."""
+    for path in bench.KERNEL_SOURCES:
+        with open(os.path.join(bench.ROOT, path)) as f:
+            text = f.read()
+        for name in ("specdec_beam_select", "specdec_reorder_states", "specdec_commit_path", "specdec_plan_slots"):
+            assert name not in text, (path, name)
