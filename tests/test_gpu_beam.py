@@ -261,7 +261,10 @@ def test_masks_of_finite_values(torch_, ver, dtype, low):
 @pytest.mark.parametrize("at", [3e4, 65530.0, 65536.0, 7e4, 9.9e5, 1.1e6, 1e8, 1e9, 2.5e9, 1e10, 1e15, 1e20, 1e30, 1e36, 1.01e37])
 def test_far_references(torch_, ver, dtype, at):
     """Rows around any finite value, of either sign: close to it, spread around
-    it, of nothing but it, and in stretches of it among ordinary logits."""
+    it, of nothing but it, and in stretches of it among ordinary logits.  The
+    tolerance is the same: the rounding of E is part of the reference, and from
+    2^16 on d = l - ref is exact where its term does not vanish (l within a factor
+    2 of ref), which leaves the one rounding of d c."""
     rng = np.random.default_rng(24)
     for W, V in ((2, 3000), (3, 7000), (3, 30000)):
         x = rng.standard_normal((6, W, V)) * 2.0
